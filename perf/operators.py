@@ -205,8 +205,9 @@ def _quantize(t, rows):
     M, K = t.shape
     blocks = _blocks(t, rows)
     most = blocks.abs().amax(dim=(1, 3))
-    inverse = torch.where(most > 0, E4M3_MAX / most, torch.ones_like(most))
-    scales = torch.where(most > 0, most / E4M3_MAX, torch.ones_like(most))
+    top = torch.full_like(most, E4M3_MAX)  # a tensor: a plain number would be multiplied with a rounded reciprocal
+    inverse = torch.where(most > 0, top / most, torch.ones_like(most))
+    scales = torch.where(most > 0, most / top, torch.ones_like(most))
     q = (blocks * inverse[:, None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return q.reshape(q.shape[0] * rows, -1)[:M, :K].contiguous(), scales
 
