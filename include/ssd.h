@@ -310,6 +310,162 @@ typedef struct {
 } ssd_plan_t;
 SSD_API ssd_status_t ssd_fwd_plan(const ssd_problem_t *prob, ssd_plan_t *plan);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the SSD in a state-space layer: the selective scan
+ * (a decay per channel and state) with its short causal convolution, the group
+ * norm with its gate, and the projections in 8-bit floating point.
+ *
+ * Tensors of tokens are rows of `channels` contiguous elements; the row of
+ * token t of sequence b starts at element b*seq + t*tok of the tensor, so a
+ * column slice of wider rows needs no copy. Strides are in elements and may be
+ * any (outputs' rows must not overlap). Pointers need the alignment of their
+ * element only; rows on 16-byte boundaries run faster.
+ *
+ * `workspace` holds the 256-byte header that ssd_fwd_check reads (the device
+ * status of the calls queued before) and, for the scan, what
+ * ssd_selective_scan_workspace_size adds. Zero-fill it once before its first
+ * use; calls on one stream may reuse it back to back, calls that may overlap
+ * need separate ones. Do not share it with ssd_fwd's calls.
+ * ------------------------------------------------------------------------ */
+
+/* Selective scan ("Mamba hardware-aware algorithms", fused selective scan): for every
+ * sequence and channel c with group g = c / (channels / ngroups),
+ *   dt_t   = softplus(dt_raw[t,c] + dt_bias[c])          (softplus = 0: without it)
+ *   h_t[n] = exp(dt_t * A[c,n]) * h_{t-1}[n] + dt_t * x[t,c] * B[t,g,n]
+ *   y[t,c] = (sum_n h_t[n] * C[t,g,n] + D[c] * x[t,c]) * z[t,c] * sigmoid(z[t,c])
+ * (no z: without the last two factors), in fp32, with the states in the state
+ * dtype where they enter and leave. seqlen 1 advances cached states by one
+ * token. */
+typedef struct {
+    int64_t batch;      /* sequences, >= 0                                       */
+    int64_t seqlen;     /* tokens of each sequence (packed: of all together), >= 0 */
+    int64_t channels;   /* >= 1                                                  */
+    int64_t dstate;     /* N, 1 .. 256                                           */
+    int64_t ngroups;    /* G, divides channels                                   */
+    int32_t io_dtype;   /* ssd_dtype_t of x, dt_raw, B, C, z, y                  */
+    int32_t state_dtype;/* SSD_F32 or SSD_F16                                    */
+    int32_t packed;     /* 1: the sequences lie one after the other on one axis of
+                           seqlen tokens, sequence s on [cu_seqlens[s], cu_seqlens[s+1]) */
+    int32_t softplus;   /* 0 or 1                                                */
+} ssd_scan_problem_t;
+
+typedef struct {
+    const void *x;            /* [batch, seqlen, channels]; packed: [1, seqlen, channels] */
+    const void *dt_raw;       /* as x                                          */
+    const void *z;            /* as x, or NULL: no gate                        */
+    const void *B, *C;        /* [batch, seqlen, ngroups, dstate], a token's G*N contiguous */
+    void *y;                  /* as x                                          */
+    const float *A;           /* [channels, dstate] contiguous                 */
+    const float *dt_bias;     /* [channels] or NULL                            */
+    const float *D;           /* [channels] or NULL                            */
+    const void *init_states;  /* [batch, channels, dstate] contiguous, or NULL: zeros */
+    void *final_states;       /* the same, or NULL: not written; may be init_states itself */
+    const int32_t *cu_seqlens;/* packed: device int32 [batch + 1], 0 = first, seqlen = last,
+                                 non-decreasing; else NULL                     */
+    int64_t x_seq, x_tok, dt_seq, dt_tok, z_seq, z_tok, b_seq, b_tok, c_seq, c_tok, y_seq, y_tok;
+} ssd_scan_tensors_t;
+
+/* Malformed offsets are seen on the device: nothing outside the tensors is
+ * touched, the outputs are undefined and ssd_fwd_check reports
+ * SSD_ERR_INVALID_ARG. Errors: SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED
+ * (dstate > 256), SSD_ERR_WORKSPACE, SSD_ERR_CUDA. */
+SSD_API ssd_status_t ssd_selective_scan_workspace_size(const ssd_scan_problem_t *prob, size_t *bytes);
+SSD_API ssd_status_t ssd_selective_scan(const ssd_scan_problem_t *prob, const ssd_scan_tensors_t *t, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/* Causal depthwise convolution over the tokens, by itself (ssd_fwd_conv has it
+ * in front of the SSD):
+ *   out[t,c] = act(bias[c] + sum_j weight[c,j] * x[t - (width-1) + j, c])
+ * with the inputs before a sequence from its cache, and the last width-1
+ * inputs of every sequence left in the cache for the next call. seqlen 1 is
+ * the decode step. */
+typedef struct {
+    int64_t batch, seqlen, channels; /* as for the scan                       */
+    int32_t width;       /* taps k, 1 .. 8                                     */
+    int32_t activation;  /* ssd_activation_t                                   */
+    int32_t io_dtype;    /* ssd_dtype_t of x, out and the cache                */
+    int32_t packed;      /* as for the scan                                    */
+} ssd_conv_problem_t;
+
+typedef struct {
+    const void *x;             /* [batch, seqlen, channels]; packed: [1, seqlen, channels] */
+    void *out;                 /* as x; must not overlap x                     */
+    const float *weight;       /* [channels, width] contiguous (tap width-1 on the current token) */
+    const float *bias;         /* [channels] or NULL                           */
+    const void *conv_state;    /* [batch, channels, width-1] contiguous, or NULL: zeros */
+    void *conv_state_out;      /* the same, or NULL: not written; may be conv_state itself */
+    const int32_t *cu_seqlens; /* as for the scan                              */
+    int64_t x_seq, x_tok, out_seq, out_tok;
+} ssd_conv_tensors_t;
+
+/* workspace: 256 bytes (the status header), or NULL: device errors go unreported. */
+SSD_API ssd_status_t ssd_conv(const ssd_conv_problem_t *prob, const ssd_conv_tensors_t *t, void *workspace,
+                              void *stream);
+
+/* Group norm with an activation, channels last. Every token is normalised by
+ * itself (so the operator is causal), each of `ngroups` groups of
+ * channels / ngroups channels with its own statistics, in fp32:
+ *   norm(v) = (v - mean(v)) / sqrt(var(v) + eps)      center = 1
+ *             v / sqrt(mean(v^2) + eps)               center = 0
+ *   no z:                 y = act(norm(x) * weight + bias)
+ *   z, gate_first = 0:    y = (norm(x) * weight + bias) * act(z)
+ *   z, gate_first = 1:    y = norm(x * act(z)) * weight + bias
+ * With `scales` the output is in e4m3 with one fp32 scale per token and 128
+ * channels, as ssd_fp8_quantize of the unrounded y gives it, ready for
+ * ssd_fp8_matmul; channels / ngroups must then be a multiple of 128, or
+ * ngroups 1. */
+typedef struct {
+    int64_t rows;        /* tokens, >= 0                                       */
+    int64_t channels;    /* >= 1                                               */
+    int64_t ngroups;     /* divides channels                                   */
+    int32_t io_dtype;    /* ssd_dtype_t of x, z and (without scales) y         */
+    int32_t activation;  /* ssd_activation_t                                   */
+    int32_t center;      /* 0 or 1                                             */
+    int32_t gate_first;  /* 0 or 1 (0 without z)                               */
+    float eps;           /* >= 0                                               */
+    int32_t reserved;    /* must be 0                                          */
+} ssd_norm_problem_t;
+
+typedef struct {
+    const void *x;        /* [rows, channels], row r at element r * x_row      */
+    const void *z;        /* the same, or NULL: no gate                        */
+    void *y;              /* [rows, channels]; e4m3 bytes with scales; may be x or z (same type and stride) */
+    float *scales;        /* [rows, ceil(channels / 128)] contiguous, or NULL  */
+    const float *weight;  /* [channels] or NULL: ones                          */
+    const float *bias;    /* [channels] or NULL: zeros                         */
+    int64_t x_row, z_row, y_row;
+} ssd_norm_tensors_t;
+
+SSD_API ssd_status_t ssd_group_norm(const ssd_norm_problem_t *prob, const ssd_norm_tensors_t *t, void *workspace,
+                                    void *stream);
+
+/* e4m3 values with one fp32 scale per block of block_rows x 128 elements of
+ * x [rows, cols]: with m the block's largest magnitude, scale = m / 448 and
+ * q = round-to-nearest-even(x * (448 / m)) (m = 0: scale 1). A block that holds
+ * an infinity or a NaN gets the scale NaN. block_rows is 1 (activations: one
+ * scale per token and 128 channels) or 128 (weights). q [rows, cols] and
+ * scales [ceil(rows / block_rows), ceil(cols / 128)] are contiguous. */
+SSD_API ssd_status_t ssd_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, int32_t io_dtype, const void *x,
+                                      int64_t x_row, void *q, float *scales, void *workspace, void *stream);
+
+/* Product of two e4m3 matrices with block scales, fp32 accumulation:
+ *   out[m,n] = bias[n] + sum_j a_scales[m,j] * b_scales[n/128,j] * sum_{k in block j} a[m,k] * b[n,k]
+ *  a         [m, k] e4m3, rows k bytes apart, 16-byte aligned;  a_scales [m, ceil(k/128)]
+ *  b         [n, k] e4m3, likewise;  b_scales [ceil(n/128), ceil(k/128)]
+ *  bias      [n] fp32 or NULL
+ *  out       [m, n] of out_dtype, row r at element r * out_row
+ * k must be a multiple of 16 (SSD_ERR_UNSUPPORTED otherwise): the copies that
+ * feed the tensor cores move 16-byte pieces. workspace: 256 bytes, required. */
+typedef struct {
+    int64_t m, n, k;     /* >= 0                                               */
+    int32_t out_dtype;   /* ssd_dtype_t                                        */
+    int32_t reserved;    /* must be 0                                          */
+} ssd_matmul_problem_t;
+
+SSD_API ssd_status_t ssd_fp8_matmul(const ssd_matmul_problem_t *prob, const void *a, const float *a_scales,
+                                    const void *b, const float *b_scales, const float *bias, void *out,
+                                    int64_t out_row, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static text for a status code. */
 SSD_API const char *ssd_status_string(ssd_status_t status);
 

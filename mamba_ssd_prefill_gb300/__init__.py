@@ -16,7 +16,8 @@ import threading
 import torch
 
 __all__ = ["ssd_fwd", "ssd_fwd_host", "ssd_fwd_varlen", "ssd_fwd_conv", "workspace_size", "make_problem", "check", "debug_set", "debug_knobs", "kernel_for", "plan_info", "SsdError",
-           "Workspace", "lib", "LIB_PATH", "STATUS"]
+           "Workspace", "lib", "LIB_PATH", "STATUS", "ssd_selective_scan", "ssd_conv", "ssd_group_norm",
+           "ssd_fp8_quantize", "ssd_fp8_matmul"]
 
 # MAMBA_SSD_LIB selects another build of the library (the bounds-checked debug build, libmamba_ssd_checked.so)
 LIB_PATH = os.environ.get("MAMBA_SSD_LIB") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmamba_ssd.so")
@@ -87,6 +88,19 @@ def lib():
             L.ssd_fwd_kernel_for.restype = ctypes.c_int
             L.ssd_fwd_plan.argtypes = [pp, ctypes.POINTER(SsdPlan)]
             L.ssd_fwd_plan.restype = ctypes.c_int
+            # the operators around the SSD (layer.py): problems and tensors as packed bytes
+            L.ssd_selective_scan_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+            L.ssd_selective_scan_workspace_size.restype = ctypes.c_int
+            L.ssd_selective_scan.argtypes = [vp, vp, vp, sz, vp]
+            L.ssd_selective_scan.restype = ctypes.c_int
+            L.ssd_conv.argtypes = [vp, vp, vp, vp]
+            L.ssd_conv.restype = ctypes.c_int
+            L.ssd_group_norm.argtypes = [vp, vp, vp, vp]
+            L.ssd_group_norm.restype = ctypes.c_int
+            L.ssd_fp8_quantize.argtypes = [i64, i64, ctypes.c_int32, ctypes.c_int32, vp, i64, vp, vp, vp, vp]
+            L.ssd_fp8_quantize.restype = ctypes.c_int
+            L.ssd_fp8_matmul.argtypes = [vp] * 7 + [i64, vp, sz, vp]
+            L.ssd_fp8_matmul.restype = ctypes.c_int
             L.ssd_status_string.argtypes = [ctypes.c_int]
             L.ssd_status_string.restype = ctypes.c_char_p
             L.ssd_version.argtypes = []
@@ -403,3 +417,6 @@ def debug_knobs(tc_heads_per_unit=-1, tc_late_ticket=-1, simt_two_pass=-1, conv_
                                int(tc_segment_chunks), int(tc_head_flags))
     if st:
         raise SsdError(st, "ssd_debug_knobs")
+
+
+from .layer import ssd_conv, ssd_fp8_matmul, ssd_fp8_quantize, ssd_group_norm, ssd_selective_scan  # noqa: E402

@@ -302,6 +302,8 @@ ssd_status_t run(const ssd_problem_t *prob, int64_t nseq, const int32_t *cu_seql
 }  // namespace
 
 namespace ssd {
+int device_sms() { return sm_count(); }
+
 ssd_status_t workspace_bytes(const ssd_problem_t *prob, bool segments, size_t *bytes) {
     Plan pl;
     const ssd_status_t st = plan(prob, -1, &pl, segments);
@@ -490,6 +492,6 @@ SSD_API const char *ssd_status_string(ssd_status_t status) {
     return "unknown status";
 }
 
-SSD_API int ssd_version(void) { return 10100; }
+SSD_API int ssd_version(void) { return 10200; }
 
 }  // extern "C"

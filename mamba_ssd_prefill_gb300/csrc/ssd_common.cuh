@@ -54,6 +54,10 @@ enum BoundsSite : uint32_t {
     SITE_CONV_IN = 131, SITE_CONV_OUT = 132, SITE_CONV_STATE = 133,
     SITE_SEG_DT = 141, SITE_SEG_BLK = 142, SITE_SEG_DECAY = 143, SITE_SEG_STATE = 144, SITE_SEG_INIT = 145,
     SITE_SEG_TMA = 146,
+    SITE_SCAN_IN = 151, SITE_SCAN_Y = 152, SITE_SCAN_STATE = 153, SITE_SCAN_SEG = 154,
+    SITE_RCONV_IN = 161, SITE_RCONV_OUT = 162, SITE_RCONV_STATE = 163,
+    SITE_NORM_IN = 171, SITE_NORM_OUT = 172, SITE_NORM_SCALE = 173,
+    SITE_FP8_IN = 181, SITE_FP8_OUT = 182, SITE_FP8_SCALE = 183,
 };
 
 // Parameters common to the kernels. Element strides are implied by the packed

@@ -71,4 +71,68 @@ struct SegPlan {
 cudaError_t launch_segstate(const Params &p, const SegPlan &sp, int io_dtype, int state_dtype, int sms,
                             cudaStream_t stream);
 
+// ---- the operators around the SSD (ssd_layer_api.cu checks their arguments) ----
+
+int device_sms();  // SM count of the current device, 0 when it cannot be read (ssd_api.cu)
+
+// Packed or regular sequences of T tokens in all; strides in elements.
+struct ScanParams {
+    const void *x, *dt, *z, *B, *C;
+    void *y;
+    const float *A, *dt_bias, *D;
+    const void *init;
+    void *fin;
+    const int32_t *cu;  // packed: [nseq + 1]; null for a regular batch
+    WsHeader *hdr;
+    int64_t nseq, L, T, D_, N, G, cpg;  // L: tokens of a sequence (packed: T); cpg: channels per group
+    int64_t x_seq, x_tok, dt_seq, dt_tok, z_seq, z_tok, b_seq, b_tok, c_seq, c_tok, y_seq, y_tok;
+    int softplus;
+};
+cudaError_t launch_scan(const ScanParams &p, int io_dtype, int state_dtype, int sms, cudaStream_t stream);
+
+struct RowConvParams {
+    const void *x;
+    void *out;
+    const float *w, *bias;
+    const void *state;
+    void *state_out;
+    const int32_t *cu;
+    WsHeader *hdr;  // may be null
+    int64_t nseq, L, T, D;
+    int64_t x_seq, x_tok, out_seq, out_tok;
+    int k, silu;
+};
+cudaError_t launch_row_conv(const RowConvParams &p, int io_dtype, int sms, cudaStream_t stream);
+
+struct NormParams {
+    const void *x, *z;
+    void *y;
+    float *scales;
+    const float *w, *bias;
+    WsHeader *hdr;  // may be null
+    int64_t rows, D, G, x_row, z_row, y_row;
+    int center, gate_first, silu;
+    float eps;
+};
+cudaError_t launch_norm(const NormParams &p, int io_dtype, int sms, cudaStream_t stream);
+
+struct QuantParams {
+    const void *x;
+    uint8_t *q;
+    float *scales;
+    WsHeader *hdr;  // may be null
+    int64_t rows, cols, x_row;
+    int block_rows;
+};
+cudaError_t launch_quantize(const QuantParams &p, int io_dtype, int sms, cudaStream_t stream);
+
+struct MatmulParams {
+    const uint8_t *a, *b;
+    const float *sa, *sb, *bias;
+    void *out;
+    WsHeader *hdr;
+    int64_t m, n, k, out_row;
+};
+cudaError_t launch_matmul(const MatmulParams &p, int out_dtype, int sms, cudaStream_t stream);
+
 }  // namespace ssd
