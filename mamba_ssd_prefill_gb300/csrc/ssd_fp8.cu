@@ -1,8 +1,5 @@
-// Projections in e4m3 with a scale per block of 128 (include/ssd.h has the formulas): the quantiser and the product.
-//
-// First form of the product: 64 x 64 tiles in shared memory, fp32 arithmetic on the CUDA cores.
-#include <cuda_fp8.h>
-
+// The quantiser of the e4m3 projections: one scale per block of 128 columns and one row (activations) or 128 rows
+// (weights); include/ssd.h has the formulas.
 #include "ssd_internal.h"
 #include "ssd_layer.cuh"
 
@@ -34,61 +31,6 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantParams p) {
     }
 }
 
-constexpr int TM = 64, TN = 64, TK = 32;
-
-__device__ __forceinline__ float from_e4m3(uint8_t v) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
-}
-
-template <typename OUT>
-__global__ void __launch_bounds__(256) matmul_kernel(MatmulParams p) {
-    __shared__ float sa[TK][TM + 1], sb[TK][TN + 1];
-    const int64_t m0 = (int64_t)blockIdx.y * TM, n0 = (int64_t)blockIdx.x * TN, kb = (p.k + 127) / 128;
-    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < p.k; k0 += TK) {
-        for (int i = tid; i < TM * TK; i += 256) {
-            const int r = i / TK, c = i % TK;
-            const bool inA = m0 + r < p.m && k0 + c < p.k, inB = n0 + r < p.n && k0 + c < p.k;
-            sa[c][r] = inA ? from_e4m3(p.a[(m0 + r) * p.k + k0 + c]) * p.sa[(m0 + r) * kb + k0 / 128] : 0.f;
-            sb[c][r] = inB ? from_e4m3(p.b[(n0 + r) * p.k + k0 + c]) * p.sb[(n0 + r) / 128 * kb + k0 / 128] : 0.f;
-        }
-        __syncthreads();
-        for (int c = 0; c < TK; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[c][ty + i * 16], sb[c][tx + j * 16], acc[i][j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + i * 16, n = n0 + tx + j * 16;
-            if (m < p.m && n < p.n)
-                *chk(static_cast<OUT *>(p.out), m * p.out_row + n, 1, (p.m - 1) * p.out_row + p.n, p.hdr,
-                     SITE_FP8_OUT) = from_f32<OUT>(acc[i][j] + (p.bias ? p.bias[n] : 0.f));
-        }
-}
-
-template <typename OUT>
-cudaError_t launch_t(const MatmulParams &p, cudaStream_t stream) {
-    const int64_t my = (p.m + TM - 1) / TM;
-    for (int64_t y = 0; y < my; y += 65535) {
-        MatmulParams q = p;
-        q.a += y * TM * p.k;
-        q.sa += y * TM * ((p.k + 127) / 128);
-        q.m -= y * TM;
-        q.out = static_cast<OUT *>(p.out) + y * TM * p.out_row;
-        matmul_kernel<OUT><<<dim3((unsigned)((p.n + TN - 1) / TN), (unsigned)std::min<int64_t>(my - y, 65535)), 256, 0,
-                             stream>>>(q);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
 }  // namespace
 
 cudaError_t launch_quantize(const QuantParams &p, int io_dtype, int sms, cudaStream_t stream) {
@@ -101,12 +43,6 @@ cudaError_t launch_quantize(const QuantParams &p, int io_dtype, int sms, cudaStr
     else
         quantize_kernel<__half><<<(unsigned)grid, 256, 0, stream>>>(p);
     return cudaGetLastError();
-}
-
-cudaError_t launch_matmul(const MatmulParams &p, int out_dtype, int, cudaStream_t stream) {
-    if (out_dtype == SSD_F32) return launch_t<float>(p, stream);
-    if (out_dtype == SSD_BF16) return launch_t<__nv_bfloat16>(p, stream);
-    return launch_t<__half>(p, stream);
 }
 
 }  // namespace ssd
