@@ -86,9 +86,18 @@ struct ScanParams {
     WsHeader *hdr;
     int64_t nseq, L, T, D_, N, G, cpg;  // L: tokens of a sequence (packed: T); cpg: channels per group
     int64_t x_seq, x_tok, dt_seq, dt_tok, z_seq, z_tok, b_seq, b_tok, c_seq, c_tok, y_seq, y_tok;
-    int softplus;
+    int softplus, state_f16;
+    int vec, vec_bc, vec_state;  // 8-channel vectors of x, dt, z, y, 4-state vectors of B, C, and states are aligned
+    int64_t rows;                // leading dimension of the token tensors (packed: 1)
+    // segments of seg_len tokens: nseg per sequence, packed: of the packed axis; the leaving states [seg_items, D, N] and
+    // summed dt [seg_items, D] of all but each last one
+    int64_t nseg, seg_len, seg_items;
+    float *seg_state, *seg_dt;
 };
-cudaError_t launch_scan(const ScanParams &p, int io_dtype, int state_dtype, int sms, cudaStream_t stream);
+// ssd_selscan.cuh, one translation unit per type
+cudaError_t launch_scan_f32(const ScanParams &p, cudaStream_t stream);
+cudaError_t launch_scan_bf16(const ScanParams &p, cudaStream_t stream);
+cudaError_t launch_scan_f16(const ScanParams &p, cudaStream_t stream);
 
 struct RowConvParams {
     const void *x;

@@ -44,6 +44,37 @@ ssd_status_t check_scan(const ssd_scan_problem_t *p) {
     return SSD_OK;
 }
 
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// Segments of a scan and where their buffers lie in the workspace.
+struct ScanPlan {
+    int64_t nseg = 1, seg_len = 0, items = 0;  // items: segments whose leaving state is kept
+    size_t state_off = 0, dt_off = 0, copy_off = 0, bytes = sizeof(WsHeader);
+};
+ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments) {
+    ScanPlan pl;
+    const int64_t chains = p.packed ? 1 : p.batch;
+    pl.seg_len = std::max<int64_t>(p.seqlen, 1);
+    if (!segments || p.batch == 0 || (!p.packed && p.seqlen <= 1)) return pl;
+    const int64_t ct = p.dstate <= 32 ? 64 : p.dstate <= 64 ? 32 : p.dstate <= 128 ? 16 : 8;
+    const int64_t ctas = chains * p.ngroups * ((p.channels / p.ngroups + ct - 1) / ct);
+    int64_t want = (2 * (int64_t)sms + ctas - 1) / ctas;
+    want = std::min<int64_t>(want, p.seqlen / 128);
+    if (ctas >= sms || want < 2) return pl;
+    int64_t len = (p.seqlen + want - 1) / want;
+    len = (len + 31) / 32 * 32;
+    pl.nseg = (p.seqlen + len - 1) / len;
+    pl.seg_len = len;
+    if (pl.nseg < 2) return pl;
+    pl.items = chains * (pl.nseg - 1);
+    const size_t dn = (size_t)(p.channels * p.dstate);
+    pl.state_off = sizeof(WsHeader);
+    pl.dt_off = align_up(pl.state_off + (size_t)pl.items * dn * 4, 256);
+    pl.copy_off = align_up(pl.dt_off + (size_t)(pl.items * p.channels) * 4, 256);
+    pl.bytes = align_up(pl.copy_off + (size_t)p.batch * dn * elem_size(p.state_dtype), 256);
+    return pl;
+}
+
 }  // namespace
 
 extern "C" {
@@ -52,7 +83,7 @@ SSD_API ssd_status_t ssd_selective_scan_workspace_size(const ssd_scan_problem_t 
     if (!bytes) return SSD_ERR_INVALID_ARG;
     const ssd_status_t st = check_scan(prob);
     if (st != SSD_OK) return st;
-    *bytes = sizeof(WsHeader);
+    *bytes = plan_scan(*prob, std::max(1, ssd::device_sms()), true).bytes;
     return SSD_OK;
 }
 
@@ -133,7 +164,46 @@ SSD_API ssd_status_t ssd_selective_scan(const ssd_scan_problem_t *prob, const ss
     p.y_seq = t->y_seq;
     p.y_tok = t->y_tok;
     p.softplus = pr.softplus;
-    return ssd::launch_scan(p, pr.io_dtype, pr.state_dtype, sms, s) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    p.state_f16 = pr.state_dtype == SSD_F16;
+    p.rows = rows_seq;
+    ScanPlan pl = plan_scan(pr, sms, true);
+    if (workspace_bytes < pl.bytes) pl = plan_scan(pr, sms, false);  // too small for segments: one chain a sequence
+    char *ws = static_cast<char *>(workspace);
+    p.nseg = pl.nseg;
+    p.seg_len = pl.seg_len;
+    p.seg_items = pl.items;
+    p.seg_state = reinterpret_cast<float *>(ws + pl.state_off);
+    p.seg_dt = reinterpret_cast<float *>(ws + pl.dt_off);
+    const int64_t vec = 16 / (int64_t)es;  // 16-byte rows of channels
+    auto rows16 = [&](const void *q, int64_t seq, int64_t tok) {
+        return !q || (aligned(q, 16) && (rows_seq <= 1 || seq % vec == 0) && (pr.seqlen <= 1 || tok % vec == 0));
+    };
+    p.vec = rows16(p.x, p.x_seq, p.x_tok) && rows16(p.dt, p.dt_seq, p.dt_tok) && rows16(p.z, p.z_seq, p.z_tok) &&
+            rows16(p.y, p.y_seq, p.y_tok) && (pr.ngroups == 1 || p.cpg % vec == 0);
+    auto states4 = [&](const void *q, int64_t seq, int64_t tok) {  // four states of B and C, or of a whole R of a step
+        const size_t a = pr.dstate > 128 ? 8 * es : 4 * es;
+        return aligned(q, a) && (rows_seq <= 1 || seq * es % a == 0) && (pr.seqlen <= 1 || tok * es % a == 0) &&
+               pr.dstate * es % a == 0;
+    };
+    p.vec_bc = states4(p.B, p.b_seq, p.b_tok) && states4(p.C, p.c_seq, p.c_tok);
+    const size_t sa = (pr.dstate > 128 ? 8 : 4) * ses;
+    p.vec_state = aligned(p.init, std::min<size_t>(sa, 16)) && aligned(p.fin, std::min<size_t>(sa, 16)) &&
+                  pr.dstate * ses % sa == 0;
+    // a segment's CTA may read a sequence's initial state after another one wrote its final state: where the two
+    // share memory the initial states are copied first
+    if (pl.nseg > 1 && p.init && p.fin) {
+        const size_t n = (size_t)(pr.batch * pr.channels * pr.dstate) * ses;
+        const char *a = static_cast<const char *>(p.init), *b = static_cast<const char *>(p.fin);
+        if (a < b + n && b < a + n) {
+            if (cudaMemcpyAsync(ws + pl.copy_off, p.init, n, cudaMemcpyDeviceToDevice, s) != cudaSuccess)
+                return SSD_ERR_CUDA;
+            p.init = ws + pl.copy_off;
+        }
+    }
+    const cudaError_t e = pr.io_dtype == SSD_F32    ? ssd::launch_scan_f32(p, s)
+                          : pr.io_dtype == SSD_BF16 ? ssd::launch_scan_bf16(p, s)
+                                                    : ssd::launch_scan_f16(p, s);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 SSD_API ssd_status_t ssd_conv(const ssd_conv_problem_t *prob, const ssd_conv_tensors_t *t, void *workspace,
