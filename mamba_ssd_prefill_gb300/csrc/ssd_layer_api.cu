@@ -56,13 +56,18 @@ ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments) {
     const int64_t chains = p.packed ? 1 : p.batch;
     pl.seg_len = std::max<int64_t>(p.seqlen, 1);
     if (!segments || p.batch == 0 || (!p.packed && p.seqlen <= 1)) return pl;
-    const int64_t ct = p.dstate <= 32 ? 64 : p.dstate <= 64 ? 32 : p.dstate <= 128 ? 16 : 8;
-    const int64_t ctas = chains * p.ngroups * ((p.channels / p.ngroups + ct - 1) / ct);
-    int64_t want = (2 * (int64_t)sms + ctas - 1) / ctas;
-    want = std::min<int64_t>(want, p.seqlen / 128);
-    if (ctas >= sms || want < 2) return pl;
+    // Without segments the work of a chain runs once, with them its states' part twice. So segments are cut only where
+    // the CTAs leave the SMs short of warps (under about 1.3 CTAs of 128 threads each: 4 x 4096 x 1536 x 16, 48 CTAs,
+    // 0.84 ms in one chain and 0.24 segmented; 32 x 4096 x 1536 x 16, 384 CTAs, 1.28 and 1.57 ms), and then so many that
+    // two waves of resident CTAs (640 threads an SM) fill: fewer leave a ragged wave, more pay the entry of a segment.
+    const ssd::ScanCta cta = ssd::scan_cta(p.dstate);
+    const int64_t per_group = (p.channels / p.ngroups + cta.channels - 1) / cta.channels;
+    const int64_t ctas = chains * p.ngroups * per_group, threads = ctas * cta.threads;
+    if (threads * 10 >= 13 * 128 * (int64_t)sms) return pl;
+    const int64_t want = std::min<int64_t>(2 * 640 * (int64_t)sms / threads, p.seqlen / 16);
+    if (want < 2) return pl;
     int64_t len = (p.seqlen + want - 1) / want;
-    len = (len + 31) / 32 * 32;
+    len = (len + 7) / 8 * 8;  // whole tiles
     pl.nseg = (p.seqlen + len - 1) / len;
     pl.seg_len = len;
     if (pl.nseg < 2) return pl;

@@ -3,25 +3,31 @@
 //
 //   h[n] <- exp(dt A[c, n]) h[n] + dt x[c] B[n],     y[c] = (sum_n C[n] h[n] + D[c] x[c]) z[c] sigmoid(z[c])
 //
-// Every (token, channel, state) costs one exponential and five flops, against 8 bytes per (token, channel) in 16-bit
-// types: at 16 states the special-function and issue rates bound it, not HBM. So the states stay in registers and the
-// work per element is kept to the recurrence itself:
+// Every (token, channel, state) costs one exponential and four multiply-adds, against 8 bytes per (token, channel) in
+// 16-bit types: at 16 states the FMA and special-function pipes bound it, not HBM. A packed f32x2 instruction takes two
+// cycles of a quarter's FMA pipe, an exponential four of the other and 1.5 of the issue beside it: 5.7 cycles an element
+// and quarter for the recurrence alone. So the states stay in registers, and what is around it is kept small:
 //
-//  - A CTA owns CT channels (of one group) and walks tokens in tiles of TT. A tile's x, dt, z, B and C are loaded to
-//    registers one tile ahead (16 bytes a thread and tensor), and turned into shared memory once: (dt, dt, dt x, dt x)
-//    per token and channel, ready for packed fp32 pairs, B and C in fp32. The step's softplus is so taken once per
-//    (token, channel), not once per state.
-//  - S lanes share a channel, R states each, in packed pairs (f32x2): per pair one multiply for the exponent, two
-//    exponentials, one multiply for dt x B, one fused multiply-add for h, one for y.
-//  - The sum over a channel's lanes is taken for TG tokens at once, each shuffle halving the tokens a lane holds, so
-//    that S - 1 shuffles serve S tokens.
+//  - A CTA owns CT channels (of one group) and walks tokens in tiles of TT. A tile's x, dt and z are copied to shared
+//    memory one tile ahead (16-byte asynchronous copies); each thread turns the vectors that it copied into (dt, dt x)
+//    per token and channel, B and C are kept in fp32. The softplus is so taken once per (token, channel).
+//  - A thread holds CH channels x R states in packed pairs, S lanes share the states of its channels. A shared memory
+//    load costs its bytes per lane, broadcast or not (an LDS.128 four cycles of the SM's pipe), and B and C are eight
+//    bytes for every element: with one channel a thread they took 3.4 cycles an element and bounded the kernel. CH = 4,
+//    R = 8 (128 registers, 8 warps' worth of CTAs) and CH = 2, R = 8 (96) measure the same where segments fill the GPU
+//    (16384 x 5120 x 16: 0.70 ms); where they are not needed the smaller one has more warps (32 x 4096 x 1536 x 16: 1.28
+//    against 1.75 ms) and is taken.
+//  - The sum over a channel's lanes is taken for the thread's channels at once, each shuffle halving the channels a
+//    lane holds.
 //
 // Where (sequences x channel tiles) do not fill the GPU, the tokens are cut into segments: scan_kernel<SUM> first
-// computes every segment's leaving state from a zero state and its summed dt (the state's decay over a segment is
-// exp(A sum dt), exactly), and each segment of the main pass folds the segments before it. That costs the state part
-// of the work twice. Packed sequences are segmented on the packed axis, whatever their lengths; a segment restarts
-// its chain wherever a sequence begins inside it.
+// computes every segment's leaving state from a zero state, and its summed dt (the state's decay over a segment is
+// exp(A sum dt), exactly); join_kernel turns them into the states that enter the segments, and the main pass starts
+// every segment from its own. The state part of the work is done twice. Packed sequences are segmented on the packed
+// axis, whatever their lengths; a segment restarts its chain wherever a sequence begins inside it.
 #pragma once
+
+#include <type_traits>
 
 #include "ssd_internal.h"
 #include "ssd_layer.cuh"
@@ -102,12 +108,28 @@ template <typename IO, int K> struct Raw {
         if constexpr (sizeof(IO) == 4) return __float_as_uint(v);
         else return *reinterpret_cast<const uint16_t *>(&v);
     }
-    __device__ __forceinline__ float get(int i) const {
+    __device__ __forceinline__ float2 pair(int i) const {  // elements i and i + 1, i even
         if constexpr (sizeof(IO) == 4) {
-            return __uint_as_float(w[i]);
+            return make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
+            return make_float2(__uint_as_float(w[i / 2] << 16), __uint_as_float(w[i / 2] & 0xffff0000u));
         } else {
-            const uint16_t h = (uint16_t)(i % 2 ? w[i / 2] >> 16 : w[i / 2]);
-            return to_f32(*reinterpret_cast<const IO *>(&h));
+            return __half22float2(*reinterpret_cast<const __half2 *>(&w[i / 2]));
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        const float2 v = pair(i & ~1);
+        return i & 1 ? v.y : v.x;
+    }
+    __device__ __forceinline__ void set_pair(int i, float x, float y) {
+        if constexpr (sizeof(IO) == 4) {
+            w[i] = __float_as_uint(x), w[i + 1] = __float_as_uint(y);
+        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(x, y);
+            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
 };
@@ -133,6 +155,11 @@ template <int S, int TG> __device__ __forceinline__ float reduce_lanes(float (&v
     return v[0];
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
 // The last sequence whose start is at or before packed token t (empty ones before it share its start).
 __device__ __forceinline__ int64_t seq_at(const int32_t *cu, int64_t nseq, int64_t t) {
     int64_t lo = 0, hi = nseq - 1;
@@ -144,35 +171,58 @@ __device__ __forceinline__ int64_t seq_at(const int32_t *cu, int64_t nseq, int64
     return lo;
 }
 
-template <int S_, int R_, int NT_, int TT_> struct Shape {
-    static constexpr int S = S_, R = R_, NT = NT_, TT = TT_;
-    static constexpr int CT = NT / S, NP = S * R, TG = S < 8 ? S : 8, CV = CT / 8;
-    static constexpr int VPT = (TT * CV + NT - 1) / NT;         // vectors of 8 channels a thread loads per tensor
-    static constexpr int NV = NP / 4;                           // vectors of 4 states per token
-    static constexpr int YS = CT + 8;                           // row of y: tokens of a reduction on different banks
-    static constexpr size_t smem(bool sum) {
-        return (size_t)TT * CT * 16 + (size_t)TT * NP * 4 * (sum ? 1 : 2) + (sum ? 0 : (size_t)TT * YS * 4) + CT * 8;
+template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_ = 512 / NT_> struct Shape {
+    static constexpr int S = S_, R = R_, CH = CH_, NT = NT_, TT = TT_, MINB = MINB_;
+    static constexpr int CT = NT / S * CH, NP = S * R, CV = CT / 8;  // channels, states, 8-channel vectors of a CTA
+    static constexpr int VPT = (TT * CV + NT - 1) / NT;              // vectors a thread copies per tensor
+    static constexpr int NV = NP / 4;                                // 4-state vectors per token
+    static constexpr size_t smem(bool sum, size_t es) {
+        return (size_t)TT * CT * (8 + (sum ? 0 : 4)) + (size_t)TT * NP * 4 * (sum ? 1 : 2) +
+               2 * (size_t)TT * CT * es * (sum ? 2 : 3) + CT * 8;
     }
 };
 
+// v[c], the shares of a thread's CH channels in each of their S lanes -> totals: lane q is left with channels q CH / S
+// onwards, CH / S of them (one where S >= CH) in v[0 ..].
+template <int S, int CH> __device__ __forceinline__ void reduce_channels(float (&v)[CH], int q) {
+    int m = CH;
+#pragma unroll
+    for (int o = S / 2; o > 0; o /= 2) {
+        if (m > 1) {
+            m /= 2;
+            const bool upper = q & o;
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i)
+                if (i < m) {
+                    const float send = upper ? v[i] : v[i + m], keep = upper ? v[i + m] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+}
+
 template <typename IO, typename T, bool SUM>
-__global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
-    constexpr int S = T::S, R = T::R, NT = T::NT, TT = T::TT, CT = T::CT, NP = T::NP, TG = T::TG, CV = T::CV,
-                  VPT = T::VPT, NV = T::NV, YS = T::YS;
+__global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
+    constexpr int S = T::S, R = T::R, NT = T::NT, TT = T::TT, CT = T::CT, NP = T::NP, CV = T::CV, VPT = T::VPT,
+                  NV = T::NV, P = R / 2, kCH = T::CH;
     constexpr int BPT = (TT * NV * (SUM ? 1 : 2) + NT - 1) / NT;
+    constexpr int RAW = TT * CT;  // elements of a staged tensor
     extern __shared__ __align__(16) uint8_t smem[];
-    ulonglong2 *du = reinterpret_cast<ulonglong2 *>(smem);                 // [TT][CT] (dt, dt, dt x, dt x)
-    float *Bs = reinterpret_cast<float *>(smem + (size_t)TT * CT * 16);    // [TT][NP]
+    float4 *du = reinterpret_cast<float4 *>(smem);                         // [TT][CT / 2] (dt, dt x) of two channels
+    float *Bs = reinterpret_cast<float *>(smem + (size_t)TT * CT * 8);     // [TT][NP]
     float *Cs = Bs + TT * NP;                                              // [TT][NP], not for SUM
-    float *ys = SUM ? Cs : Cs + TT * NP;                                   // [TT][YS], not for SUM
-    float *bias_s = SUM ? ys : ys + TT * YS, *D_s = bias_s + CT;           // [CT] each
+    float *ys = SUM ? Cs : Cs + TT * NP;                                   // [TT][CT], not for SUM
+    float *bias_s = SUM ? ys : ys + TT * CT, *D_s = bias_s + CT;           // [CT] each
+    IO *raw = reinterpret_cast<IO *>(D_s + CT);                            // [2][x, dt, z][TT][CT]
     const int tid = threadIdx.x;
     const int64_t per_group = (p.cpg + CT - 1) / CT, ctiles = per_group * p.G;
     const int64_t item = blockIdx.x / ctiles, ct = blockIdx.x % ctiles, g = ct / per_group;
     const int64_t c0 = g * p.cpg + ct % per_group * CT;                    // first channel
-    const int64_t left = (g + 1) * p.cpg - c0;                             // channels of the group from c0 on
-    const int ch = tid / S, q = tid % S;                                   // this lane's channel and place
-    const bool live = ch < left;
+    const int left = (int)((g + 1) * p.cpg - c0 < CT ? (g + 1) * p.cpg - c0 : CT);  // channels of this CTA
+    const int ch = tid / S * kCH, q = tid % S;                             // this thread's first channel, its lane's place
+    const int clive = left - ch < 0 ? 0 : left - ch < kCH ? left - ch : kCH;
     const bool packed = p.cu != nullptr;
 
     // tokens [t0, t1) of sequence `sq` (packed: of the packed axis, sq the sequence that holds t0)
@@ -186,22 +236,23 @@ __global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
         int64_t qb;
         sq = seq_at(p.cu, p.nseq, SUM ? t1 - 1 : t0);
         packed_range(p.cu, sq, p.T, qb, qe);
+        fresh = qb >= t0;
         if (SUM) {
-            if (qe <= t1) return;  // no sequence goes on past this segment
-            fresh = qb >= t0;
             if (fresh) t0 = qb < t1 ? qb : t1;
+            if (qe <= t1) {  // no sequence goes on past this segment
+                if (tid < left) p.seg_dt[item * p.D_ + c0 + tid] = __int_as_float(0x7fffffff);
+                return;
+            }
         } else {
-            fresh = qb >= t0;
             if (qe <= t0) qe = p.T;  // malformed offsets
             if (item == 0 && ct == 0) check_offsets(p.cu, p.nseq, p.T, p.hdr);
             if (p.fin)  // empty sequences keep their states; each segment's CTAs look after some of them
                 for (int64_t s = item; s < p.nseq; s += p.nseg)
                     if (p.cu[s] == p.cu[s + 1])
-                        for (int64_t e = tid; e < CT * p.N; e += NT)
-                            if (e / p.N < left) {
-                                const int64_t i = (s * p.D_ + c0) * p.N + e;
-                                store_state(p, p.fin, i, p.init ? load_state(p, p.init, i) : 0.f);
-                            }
+                        for (int64_t e = tid; e < left * p.N; e += NT) {
+                            const int64_t i = (s * p.D_ + c0) * p.N + e;
+                            store_state(p, p.fin, i, p.init ? load_state(p, p.init, i) : 0.f);
+                        }
         }
     } else {
         sq = item / nseg;
@@ -217,70 +268,10 @@ __global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
     const IO *B = static_cast<const IO *>(p.B) + row * p.b_seq + g * p.N;
     const IO *C = static_cast<const IO *>(p.C) + row * p.c_seq + g * p.N;
 
-    for (int i = tid; i < CT; i += NT) {
-        bias_s[i] = p.dt_bias && i < left ? p.dt_bias[c0 + i] : 0.f;
-        D_s[i] = p.D && i < left ? p.D[c0 + i] : 0.f;
-    }
-
-    f2 a[R / 2], h[R / 2];
-    const int64_t cN = (c0 + (live ? ch : 0)) * p.N;
-    const int n0 = q * R;
-    auto get2 = [&](auto f) {  // f(n) for this lane's states, 0 past the last and for missing channels
-#pragma unroll
-        for (int i = 0; i < R / 2; ++i) {
-            const int n = n0 + 2 * i;
-            h[i] = pack2(live && n < p.N ? f(n) : 0.f, live && n + 1 < p.N ? f(n + 1) : 0.f);
-        }
-    };
-    get2([&](int n) { return p.A[cN + n] * kLog2e; });
-#pragma unroll
-    for (int i = 0; i < R / 2; ++i) a[i] = h[i];
-    auto initial = [&](int64_t s) {
-        get2([&](int n) { return p.init ? load_state(p, p.init, s * p.D_ * p.N + cN + n) : 0.f; });
-    };
-    auto final_state = [&](int64_t s) {
-        if (p.fin && live)
-#pragma unroll
-            for (int i = 0; i < R / 2; ++i) {
-                const int n = n0 + 2 * i;
-                const float2 v = unpack2(h[i]);
-                if (n < p.N) store_state(p, p.fin, s * p.D_ * p.N + cN + n, v.x);
-                if (n + 1 < p.N) store_state(p, p.fin, s * p.D_ * p.N + cN + n + 1, v.y);
-            }
-    };
-    if (fresh) {
-        initial(sq);
-    } else if (SUM) {
-        get2([](int) { return 0.f; });
-    } else {  // the segments before, from the one in which the sequence began
-        int64_t j = 0, first = sq * (p.nseg - 1);
-        if (packed) {
-            int64_t qb, e;
-            packed_range(p.cu, sq, p.T, qb, e);
-            j = qb / p.seg_len;
-            first = 0;
-        }
-        const int64_t extent = p.seg_items * p.D_ * p.N;
-        auto leaving = [&](int64_t i, int n) {
-            return *chk(p.seg_state, (first + i) * p.D_ * p.N + cN + n, 1, extent, p.hdr, SITE_SCAN_SEG);
-        };
-        get2([&](int n) { return leaving(j, n); });
-        for (++j; j < k; ++j) {
-            const float d = live ? p.seg_dt[(first + j) * p.D_ + c0 + ch] : 0.f;
-#pragma unroll
-            for (int i = 0; i < R / 2; ++i) {
-                const int n = n0 + 2 * i;
-                const float2 e = unpack2(mul2(a[i], pack2(d, d)));
-                h[i] = fma2(pack2(ex2(e.x), ex2(e.y)), h[i],
-                            pack2(live && n < p.N ? leaving(j, n) : 0.f, live && n + 1 < p.N ? leaving(j, n + 1) : 0.f));
-            }
-        }
-    }
-
-    // loads of one tile: 8 channels of a token per vector, and 4 states of a token of B or C
-    const int cv = tid % CV, trow = tid / CV;             // channel vector and first token of this thread
-    const int clive = (int)(left - cv * 8 < 0 ? 0 : left - cv * 8 < 8 ? left - cv * 8 : 8);
-    Raw<IO, 8> rx[VPT], rd[VPT], rz[VPT];
+    // copies of one tile: vectors of 8 channels of a token; a thread later reads the vectors that it copied itself
+    const int cv = tid % CV * 8, trow = tid / CV;  // first channel of this thread's vectors, first token
+    const int vlive = left - cv < 0 ? 0 : left - cv < 8 ? left - cv : 8;
+    constexpr int TSTEP = NT / CV;
     Raw<IO, 4> rb[BPT];
     const int64_t xn = (p.rows - 1) * p.x_seq + (p.L - 1) * p.x_tok + p.D_;
     const int64_t dn = (p.rows - 1) * p.dt_seq + (p.L - 1) * p.dt_tok + p.D_;
@@ -293,94 +284,191 @@ __global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
         const IO *w = static_cast<const IO *>(whole);
         return (const IO *)chk(w, base + off - w, n, extent, p.hdr, SITE_SCAN_IN);
     };
-    auto load = [&](int64_t tile) {
+    auto copy = [&](IO *dst, const IO *src) {
+        if (p.vec && vlive == 8) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(IO) / 2; ++i)
+                cp_async16(reinterpret_cast<uint8_t *>(dst) + 16 * i, reinterpret_cast<const uint8_t *>(src) + 16 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = i < vlive ? src[i] : from_f32<IO>(0.f);
+        }
+    };
+    // element offsets of this thread's first vectors in the tile that is copied next, stepped from tile to tile
+    int64_t ox = (t0 + trow) * p.x_tok + cv, od = (t0 + trow) * p.dt_tok + cv, oz = (t0 + trow) * p.z_tok + cv;
+    const int b_t = tid / NV % TT, b_n = tid % NV * 4;
+    auto load = [&](int64_t tile, int stage) {
+        IO *st = raw + stage * (SUM ? 2 : 3) * RAW + trow * CT + cv;
+        const int n = (int)(t1 - tile < TT ? t1 - tile : TT);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int t = trow + v * (NT / CV);
-            rx[v].zero();
-            rd[v].zero();
-            rz[v].zero();
-            if ((TT * CV % NT == 0 || t < TT) && tile + t < t1 && clive > 0) {
-                const int64_t tk = tile + t;
-                rx[v].load(at(x, p.x, tk * p.x_tok + cv * 8, clive, xn), clive, p.vec);
-                rd[v].load(at(dt, p.dt, tk * p.dt_tok + cv * 8, clive, dn), clive, p.vec);
-                if (!SUM && z) rz[v].load(at(z, p.z, tk * p.z_tok + cv * 8, clive, zn), clive, p.vec);
+            const int t = trow + v * TSTEP;
+            if (t < n && vlive > 0) {
+                copy(st + v * TSTEP * CT, at(x, p.x, ox + v * TSTEP * p.x_tok, vlive, xn));
+                copy(st + RAW + v * TSTEP * CT, at(dt, p.dt, od + v * TSTEP * p.dt_tok, vlive, dn));
+                if (!SUM && z) copy(st + 2 * RAW + v * TSTEP * CT, at(z, p.z, oz + v * TSTEP * p.z_tok, vlive, zn));
             }
         }
+        ox += TT * p.x_tok;
+        od += TT * p.dt_tok;
+        if (!SUM) oz += TT * p.z_tok;
+        asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
         for (int v = 0; v < BPT; ++v) {
-            const int e = tid + v * NT, t = e / NV % TT, n = e % NV * 4, nl = (int)(p.N - n);
+            const int e = tid + v * NT, t = BPT == 1 ? b_t : e / NV % TT, n4 = BPT == 1 ? b_n : e % NV * 4;
+            const int nl = (int)(p.N - n4);
             rb[v].zero();
-            if (e < TT * NV * (SUM ? 1 : 2) && tile + t < t1 && nl > 0) {
+            if (e < TT * NV * (SUM ? 1 : 2) && t < n && nl > 0) {
                 const int64_t tk = tile + t;
-                if (SUM || e < TT * NV) rb[v].load(at(B, p.B, tk * p.b_tok + n, nl < 4 ? nl : 4, bn), nl, p.vec_bc);
-                else rb[v].load(at(C, p.C, tk * p.c_tok + n, nl < 4 ? nl : 4, cn), nl, p.vec_bc);
+                if (SUM || e < TT * NV) rb[v].load(at(B, p.B, tk * p.b_tok + n4, nl < 4 ? nl : 4, bn), nl, p.vec_bc);
+                else rb[v].load(at(C, p.C, tk * p.c_tok + n4, nl < 4 ? nl : 4, cn), nl, p.vec_bc);
             }
         }
     };
-    // slot of a channel in a row of du: 8-channel vectors written by different threads fall on different banks
-    auto slot = [](int c) { return (c & ~7) | ((c ^ (c >> 3)) & 7); };
-    const int my_slot = slot(ch);
-    float dt_sum = 0.f;
+    load(t0, 0);
 
-    // tokens [lo, hi) of the tile in shared memory; MASK: other tokens of the groups of TG leave the state alone
+    for (int i = tid; i < CT; i += NT) {
+        bias_s[i] = p.dt_bias && i < left ? p.dt_bias[c0 + i] : 0.f;
+        D_s[i] = p.D && i < left ? p.D[c0 + i] : 0.f;
+    }
+    f2 a[kCH][P], h[kCH][P];
+    const int n0 = q * R;
+    auto get2 = [&](auto f) {  // f(c, n) for this lane's channels and states, 0 past the last
+#pragma unroll
+        for (int c = 0; c < kCH; ++c)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int n = n0 + 2 * i;
+                h[c][i] = pack2(c < clive && n < p.N ? f(c0 + ch + c, n) : 0.f,
+                                c < clive && n + 1 < p.N ? f(c0 + ch + c, n + 1) : 0.f);
+            }
+    };
+    get2([&](int64_t c, int n) { return p.A[c * p.N + n] * kLog2e; });
+#pragma unroll
+    for (int c = 0; c < kCH; ++c)
+#pragma unroll
+        for (int i = 0; i < P; ++i) a[c][i] = h[c][i];
+    auto initial = [&](int64_t s) {
+        get2([&](int64_t c, int n) { return p.init ? load_state(p, p.init, (s * p.D_ + c) * p.N + n) : 0.f; });
+    };
+    auto each_state = [&](auto f) {  // f(c, n, h) for this lane's channels and states
+#pragma unroll
+        for (int c = 0; c < kCH; ++c)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int n = n0 + 2 * i;
+                const float2 v = unpack2(h[c][i]);
+                if (c < clive && n < p.N) f(c0 + ch + c, n, v.x);
+                if (c < clive && n + 1 < p.N) f(c0 + ch + c, n + 1, v.y);
+            }
+    };
+    auto final_state = [&](int64_t s) {
+        if (p.fin) each_state([&](int64_t c, int n, float v) { store_state(p, p.fin, (s * p.D_ + c) * p.N + n, v); });
+    };
+    const int64_t extent = p.seg_items * p.D_ * p.N;
+    (void)extent;
+    if (fresh) {
+        initial(sq);
+    } else if (SUM) {
+        get2([](int64_t, int) { return 0.f; });
+    } else {  // the state that enters this segment
+        const int64_t i0 = (packed ? 0 : sq * (p.nseg - 1)) + k - 1;
+        get2([&](int64_t c, int n) {
+            return *chk(p.seg_state, (i0 * p.D_ + c) * p.N + n, 1, extent, p.hdr, SITE_SCAN_SEG);
+        });
+    }
+
+    // places of a two-channel unit in a row of du, of a four-channel unit in a row of ys: threads that write and threads
+    // that read neighbouring units fall on different banks
+    auto du_at = [](int t, int unit) { return t * (CT / 2) + (unit ^ ((unit >> 3) & 3)); };
+    auto ys_at = [](int t, int unit) { return t * CT + (unit ^ ((unit >> 3) & 1)) * 4; };
+    float dt_sum[kCH] = {};
+
+    // tokens [lo, hi) of the tile in shared memory; MASK: the others leave the state alone
     auto run = [&](auto mask, int lo, int hi) {
         constexpr bool MASK = decltype(mask)::value;
-        float part_dt = 0.f;
+        float part[kCH] = {};
 #pragma unroll 2
-        for (int g0 = lo / TG * TG; g0 < hi; g0 += TG) {
-            float v[TG];
+        for (int t = MASK ? lo : 0; t < (MASK ? hi : TT); ++t) {
+            float d[kCH], u[kCH];
 #pragma unroll
-            for (int i = 0; i < TG; ++i) {
-                const int t = g0 + i;
-                const bool in = !MASK || (t >= lo && t < hi);
-                const ulonglong2 d = du[t * CT + my_slot];
-                const ulonglong2 *b = reinterpret_cast<const ulonglong2 *>(Bs + t * NP + n0);
-                const ulonglong2 *c = reinterpret_cast<const ulonglong2 *>(Cs + t * NP + n0);
+            for (int c = 0; c < kCH; c += 2) {
+                const float4 w = du[du_at(t, (ch + c) / 2)];
+                d[c] = w.x, u[c] = w.y, d[c + 1] = w.z, u[c + 1] = w.w;
+            }
+            const ulonglong2 *bp = reinterpret_cast<const ulonglong2 *>(Bs + t * NP + n0);
+            const ulonglong2 *cp = reinterpret_cast<const ulonglong2 *>(Cs + t * NP + n0);
+            f2 b[P], cc[P];
+#pragma unroll
+            for (int j = 0; j < P / 2; ++j) {
+                const ulonglong2 w = bp[j];
+                b[2 * j] = w.x;
+                b[2 * j + 1] = w.y;
+            }
+            if (!SUM)
+#pragma unroll
+                for (int j = 0; j < P / 2; ++j) {
+                    const ulonglong2 w = cp[j];
+                    cc[2 * j] = w.x;
+                    cc[2 * j + 1] = w.y;
+                }
+            float v[kCH];
+#pragma unroll
+            for (int c = 0; c < kCH; ++c) {
+                const f2 dd = pack2(d[c], d[c]), uu = pack2(u[c], u[c]);
                 f2 y = 0;
 #pragma unroll
-                for (int j = 0; j < R / 4; ++j) {
-                    const ulonglong2 bb = b[j];
-                    const float2 e0 = unpack2(mul2(d.x, a[2 * j])), e1 = unpack2(mul2(d.x, a[2 * j + 1]));
-                    const f2 h0 = fma2(pack2(ex2(e0.x), ex2(e0.y)), h[2 * j], mul2(d.y, bb.x));
-                    const f2 h1 = fma2(pack2(ex2(e1.x), ex2(e1.y)), h[2 * j + 1], mul2(d.y, bb.y));
-                    h[2 * j] = in ? h0 : h[2 * j];
-                    h[2 * j + 1] = in ? h1 : h[2 * j + 1];
-                    if (!SUM) {
-                        const ulonglong2 cc = c[j];
-                        y = j == 0 ? mul2(h[0], cc.x) : fma2(h[2 * j], cc.x, y);
-                        y = fma2(h[2 * j + 1], cc.y, y);
-                    }
+                for (int j = 0; j < P; ++j) {
+                    const float2 e = unpack2(mul2(dd, a[c][j]));
+                    h[c][j] = fma2(pack2(ex2(e.x), ex2(e.y)), h[c][j], mul2(uu, b[j]));
+                    if (!SUM) y = j == 0 ? mul2(h[c][j], cc[j]) : fma2(h[c][j], cc[j], y);
                 }
-                if (SUM) part_dt += in ? unpack2(d.x).x : 0.f;
                 const float2 yy = unpack2(y);
-                v[i] = yy.x + yy.y;
+                v[c] = yy.x + yy.y;
+                if (SUM) part[c] += d[c];
             }
             if (!SUM) {
-                const float total = reduce_lanes<S, TG>(v, q);
-                const int t = g0 + q * TG / S;
-                if ((S <= TG || q % (S / TG) == 0) && (!MASK || (t >= lo && t < hi))) ys[t * YS + ch] = total;
+                reduce_channels<S, kCH>(v, q);
+                constexpr int LEFT = S < kCH ? kCH / S : 1;  // channels left in this lane
+                const int c = ch + q * kCH / S;
+                float *o = ys + ys_at(t, c / 4) + c % 4;
+                if constexpr (LEFT == 4) *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                else if constexpr (LEFT == 2) *reinterpret_cast<float2 *>(o) = make_float2(v[0], v[1]);
+                else if (S <= kCH || q % (S / kCH) == 0) o[0] = v[0];
             }
         }
-        dt_sum += part_dt;
+        if (SUM)
+#pragma unroll
+            for (int c = 0; c < kCH; ++c) dt_sum[c] += part[c];
     };
 
-    load(t0);
-    for (int64_t tile = t0; tile < t1; tile += TT) {
+    int64_t oy = row * p.y_seq + (t0 + trow) * p.y_tok + c0 + cv;
+    int stage = 0;
+    for (int64_t tile = t0; tile < t1; tile += TT, stage ^= 1, oy += TT * p.y_tok) {
         const int n = (int)(t1 - tile < TT ? t1 - tile : TT);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (tile == t0) __syncthreads();  // bias_s and D_s
-        // (dt, dt, dt x, dt x); tokens past the end: a decay of 1 and nothing added
+        const IO *st = raw + stage * (SUM ? 2 : 3) * RAW;
+        // (dt, dt x); tokens past the end: a decay of 1 and nothing added
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int t = trow + v * (NT / CV);
+            const int t = trow + v * TSTEP;
             if (TT * CV % NT == 0 || t < TT) {
+                Raw<IO, 8> rx, rd;
+                rx.load(st + t * CT + cv);
+                rd.load(st + RAW + t * CT + cv);
+                if (t < n) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float d = rd[v].get(i) + bias_s[cv * 8 + i];
-                    if (p.softplus) d = softplus_fast(d);
-                    if (t >= n) d = 0.f;
-                    const float u = d * rx[v].get(i);
-                    du[t * CT + slot(cv * 8 + i)] = make_ulonglong2(pack2(d, d), pack2(u, u));
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 r2 = rd.pair(i), x2 = rx.pair(i);
+                        const float2 b2 = *reinterpret_cast<const float2 *>(bias_s + cv + i);
+                        float d0 = r2.x + b2.x, d1 = r2.y + b2.y;
+                        if (p.softplus) d0 = softplus_fast(d0), d1 = softplus_fast(d1);
+                        du[du_at(t, (cv + i) / 2)] = make_float4(d0, d0 * x2.x, d1, d1 * x2.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) du[du_at(t, (cv + i) / 2)] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
         }
@@ -391,10 +479,7 @@ __global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
                 *reinterpret_cast<float4 *>(Bs + e * 4) =  // C follows B
                     make_float4(rb[v].get(0), rb[v].get(1), rb[v].get(2), rb[v].get(3));
         }
-        Raw<IO, 8> cx[VPT], cz[VPT];  // this tile's x and z, for its output
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) cx[v] = rx[v], cz[v] = rz[v];
-        if (tile + TT < t1) load(tile + TT);
+        if (tile + TT < t1) load(tile + TT, stage ^ 1);
         __syncthreads();
         if (SUM || !packed || qe > tile + n) {
             run(std::integral_constant<bool, false>(), 0, TT);
@@ -424,25 +509,34 @@ __global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
         if (!SUM) {
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                const int t = trow + v * (NT / CV);
-                if (t < n && clive > 0) {
+                const int t = trow + v * TSTEP;
+                if (t < n && vlive > 0) {
+                    Raw<IO, 8> rx, rz;
+                    rx.load(st + t * CT + cv);
+                    if (z) rz.load(st + 2 * RAW + t * CT + cv);
                     float o[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        o[i] = fmaf(D_s[cv * 8 + i], cx[v].get(i), ys[t * YS + cv * 8 + i]);
-                        if (z) o[i] *= silu_f32(cz[v].get(i));
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 y4 = *reinterpret_cast<const float4 *>(ys + ys_at(t, (cv + i) / 4));
+                        const float4 D4 = *reinterpret_cast<const float4 *>(D_s + cv + i);
+                        const float2 xa = rx.pair(i), xb = rx.pair(i + 2);
+                        o[i] = fmaf(D4.x, xa.x, y4.x);
+                        o[i + 1] = fmaf(D4.y, xa.y, y4.y);
+                        o[i + 2] = fmaf(D4.z, xb.x, y4.z);
+                        o[i + 3] = fmaf(D4.w, xb.y, y4.w);
                     }
-                    IO *out = chk(static_cast<IO *>(p.y), row * p.y_seq + (tile + t) * p.y_tok + c0 + cv * 8, clive, yn,
-                                  p.hdr, SITE_SCAN_Y);
-                    if (p.vec && clive == 8) {
+                    if (z)
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const float2 g = rz.pair(i);
+                            o[i] *= silu_f32(g.x);
+                            o[i + 1] *= silu_f32(g.y);
+                        }
+                    IO *out = chk(static_cast<IO *>(p.y), oy + v * TSTEP * p.y_tok, vlive, yn, p.hdr, SITE_SCAN_Y);
+                    if (p.vec && vlive == 8) {
                         Raw<IO, 8> w;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t b = Raw<IO, 8>::bits(from_f32<IO>(o[i]));
-                            if constexpr (sizeof(IO) == 4) w.w[i] = b;
-                            else if (i % 2 == 0) w.w[i / 2] = b;
-                            else w.w[i / 2] |= b << 16;
-                        }
+                        for (int i = 0; i < 8; i += 2) w.set_pair(i, o[i], o[i + 1]);
 #pragma unroll
                         for (int i = 0; i < Raw<IO, 8>::W / 4; ++i)
                             reinterpret_cast<uint4 *>(out)[i] =
@@ -450,30 +544,44 @@ __global__ void __launch_bounds__(T::NT) scan_kernel(ScanParams p) {
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (i < clive) out[i] = from_f32<IO>(o[i]);
+                            if (i < vlive) out[i] = from_f32<IO>(o[i]);
                     }
                 }
             }
         }
     }
     if (SUM) {
-        if (live) {
-            const int64_t i0 = packed ? item : sq * (p.nseg - 1) + k;
+        const int64_t i0 = packed ? item : sq * (p.nseg - 1) + k;
+        each_state([&](int64_t c, int n, float v) {
+            *chk(p.seg_state, (i0 * p.D_ + c) * p.N + n, 1, extent, p.hdr, SITE_SCAN_SEG) = v;
+        });
+        // a segment in which a sequence begins does not take up the state before it: its sum is NaN
 #pragma unroll
-            for (int i = 0; i < R / 2; ++i) {
-                const int n = n0 + 2 * i;
-                const float2 v = unpack2(h[i]);
-                if (n < p.N) {
-                    float *s = chk(p.seg_state, i0 * p.D_ * p.N + cN + n, n + 1 < p.N ? 2 : 1,
-                                   p.seg_items * p.D_ * p.N, p.hdr, SITE_SCAN_SEG);
-                    s[0] = v.x;
-                    if (n + 1 < p.N) s[1] = v.y;
-                }
-            }
-            if (q == 0) p.seg_dt[i0 * p.D_ + c0 + ch] = dt_sum;
-        }
+        for (int c = 0; c < kCH; ++c)
+            if (q == 0 && c < clive)
+                p.seg_dt[i0 * p.D_ + c0 + ch + c] = packed && fresh ? __int_as_float(0x7fffffff) : dt_sum[c];
     } else if (!packed && t1 == p.L) {
         final_state(sq);
+    }
+}
+
+// seg_state[i], the leaving state of segment i from a zero state -> from its true entering state (which is what enters
+// segment i + 1). A thread takes one state of a channel through the segments of a sequence (packed: of the axis).
+static __global__ void __launch_bounds__(256) join_kernel(ScanParams p) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, dn = p.D_ * p.N;
+    const int64_t chains = p.cu ? 1 : p.nseq, segs = p.nseg - 1;
+    if (e >= chains * dn) return;
+    const int64_t i = e % dn, c = i / p.N, base = e / dn * segs;
+    const float a = p.A[i] * kLog2e;
+    const int64_t extent = p.seg_items * dn;
+    (void)extent;
+    float h = *chk(p.seg_state, base * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
+#pragma unroll 4
+    for (int64_t j = 1; j < segs; ++j) {
+        float *s = chk(p.seg_state, (base + j) * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
+        const float d = p.seg_dt[(base + j) * p.D_ + c], v = *s;
+        h = d != d ? v : fmaf(ex2(a * d), h, v);
+        *s = h;
     }
 }
 
@@ -592,7 +700,7 @@ cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream)
     const int64_t grid = items * ((p.cpg + T::CT - 1) / T::CT) * p.G;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     auto k = scan_kernel<IO, T, SUM>;
-    constexpr size_t smem = T::smem(SUM);
+    constexpr size_t smem = T::smem(SUM, sizeof(IO));
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -603,8 +711,15 @@ cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream)
 template <typename IO, typename T>
 cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
     if (p.nseg > 1) {
-        const cudaError_t e = launch_pass<IO, T, true>(p, p.seg_items, stream);
+        cudaError_t e = launch_pass<IO, T, true>(p, p.seg_items, stream);
         if (e != cudaSuccess) return e;
+        if (p.nseg > 2) {
+            const int64_t grid = ((p.cu ? 1 : p.nseq) * p.D_ * p.N + 255) / 256;
+            if (grid > INT32_MAX) return cudaErrorInvalidValue;
+            join_kernel<<<(unsigned)grid, 256, 0, stream>>>(p);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
     }
     return launch_pass<IO, T, false>(p, p.cu ? p.nseg : p.nseq * p.nseg, stream);
 }
@@ -617,13 +732,20 @@ cudaError_t launch_step_kernel(const ScanParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-using Shape4 = Shape<1, 4, 64, 32>;     // up to 4 states
-using Shape8 = Shape<2, 4, 128, 32>;    // up to 8
-using Shape16 = Shape<4, 4, 256, 32>;   // up to 16
-using Shape32 = Shape<4, 8, 256, 32>;
-using Shape64 = Shape<8, 8, 256, 32>;
-using Shape128 = Shape<16, 8, 256, 32>;
-using Shape256 = Shape<32, 8, 256, 16>;
+// By the number of states; scan_cta (ssd_internal.h) tells the planner their channels and threads.
+using Shape4 = Shape<1, 4, 4, 32, 8, 16>;
+using Shape8 = Shape<1, 8, 2, 64, 8, 10>;
+using Shape16 = Shape<2, 8, 2, 128, 8, 5>;
+using Shape24 = Shape<2, 12, 2, 128, 8, 4>;
+using Shape32 = Shape<4, 8, 2, 256, 8, 2>;
+using Shape64 = Shape<8, 8, 2, 256, 8, 2>;
+using Shape128 = Shape<16, 8, 2, 256, 8, 2>;
+using Shape256 = Shape<32, 8, 2, 256, 8, 2>;
+
+template <typename IO, typename T> cudaError_t launch_checked(const ScanParams &p, cudaStream_t stream) {
+    const ScanCta c = scan_cta(p.N);
+    return c.channels == T::CT && c.threads == T::NT ? launch_shape<IO, T>(p, stream) : cudaErrorInvalidValue;
+}
 
 template <typename IO> cudaError_t launch_io(const ScanParams &p, cudaStream_t stream) {
     if (!p.cu && p.L == 1) {
@@ -635,13 +757,14 @@ template <typename IO> cudaError_t launch_io(const ScanParams &p, cudaStream_t s
         if (p.N <= 128) return launch_step_kernel<IO, 32, 4>(p, stream);
         return launch_step_kernel<IO, 32, 8>(p, stream);
     }
-    if (p.N <= 4) return launch_shape<IO, Shape4>(p, stream);
-    if (p.N <= 8) return launch_shape<IO, Shape8>(p, stream);
-    if (p.N <= 16) return launch_shape<IO, Shape16>(p, stream);
-    if (p.N <= 32) return launch_shape<IO, Shape32>(p, stream);
-    if (p.N <= 64) return launch_shape<IO, Shape64>(p, stream);
-    if (p.N <= 128) return launch_shape<IO, Shape128>(p, stream);
-    return launch_shape<IO, Shape256>(p, stream);
+    if (p.N <= 4) return launch_checked<IO, Shape4>(p, stream);
+    if (p.N <= 8) return launch_checked<IO, Shape8>(p, stream);
+    if (p.N <= 16) return launch_checked<IO, Shape16>(p, stream);
+    if (p.N <= 24) return launch_checked<IO, Shape24>(p, stream);
+    if (p.N <= 32) return launch_checked<IO, Shape32>(p, stream);
+    if (p.N <= 64) return launch_checked<IO, Shape64>(p, stream);
+    if (p.N <= 128) return launch_checked<IO, Shape128>(p, stream);
+    return launch_checked<IO, Shape256>(p, stream);
 }
 
 }  // namespace scan
