@@ -39,16 +39,6 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-// Two fp32 fused multiply-adds in one instruction, each rounded like a scalar fmaf.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
-        "mov.b64 pc, {%6, %7};\n\tfma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
 // acc += s * r, 16 columns
 __device__ __forceinline__ void add16(float *acc, const uint32_t (&r)[16], float2 s) {
 #pragma unroll

@@ -121,6 +121,8 @@ struct RowConvParams {
     int64_t nseq, L, T, D;
     int64_t x_seq, x_tok, out_seq, out_tok;
     int k, silu;
+    int vec, vec_state, vec_w;  // rows of x and out, the cache left behind, and the taps lie on 16-byte boundaries
+    int64_t rows;               // leading dimension of x and out (packed: 1)
 };
 cudaError_t launch_row_conv(const RowConvParams &p, int io_dtype, int sms, cudaStream_t stream);
 
@@ -132,6 +134,7 @@ struct NormParams {
     WsHeader *hdr;  // may be null
     int64_t rows, D, G, x_row, z_row, y_row;
     int center, gate_first, silu;
+    int vec;  // 16-byte pieces of every group of x, z, y, w and bias are aligned
     float eps;
 };
 cudaError_t launch_norm(const NormParams &p, int io_dtype, int sms, cudaStream_t stream);
@@ -143,6 +146,7 @@ struct QuantParams {
     WsHeader *hdr;  // may be null
     int64_t rows, cols, x_row;
     int block_rows;
+    int vec;  // 8-element pieces of x and q are aligned
 };
 cudaError_t launch_quantize(const QuantParams &p, int io_dtype, int sms, cudaStream_t stream);
 

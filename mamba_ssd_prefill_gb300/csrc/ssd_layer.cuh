@@ -2,9 +2,23 @@
 // itself, group norm, e4m3 projections).
 #pragma once
 
+#include <type_traits>
+
 #include "ssd_common.cuh"
 
 namespace ssd {
+
+// a / b and a % b of non-negative numbers; a 64-bit division takes some ten times a 32-bit one.
+__device__ __forceinline__ int64_t quick_div(int64_t a, int64_t b, int64_t &rest) {
+    if (((a | b) >> 32) == 0) {
+        const uint32_t q = (uint32_t)a / (uint32_t)b;
+        rest = (uint32_t)a - q * (uint32_t)b;
+        return q;
+    }
+    const int64_t q = a / b;
+    rest = a - q * b;
+    return q;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -39,6 +53,88 @@ __device__ __forceinline__ float softplus_fast(float v) {
 
 // v sigmoid(v) in fp32 (a few ulp; 0 below about -88).
 __device__ __forceinline__ float silu_f32(float v) { return v * rcp(1.f + ex2(v * -kLog2e)); }
+
+// K consecutive elements as they lie, in registers
+template <typename IO, int K> struct Raw {
+    static constexpr int W = K * (int)sizeof(IO) < 4 ? 1 : K * (int)sizeof(IO) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    // all K elements; p is aligned for them
+    __device__ __forceinline__ void load(const IO *p) {
+        if constexpr (K == 1) {
+            w[0] = bits(*p);
+        } else if constexpr (W == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    // the first n of K elements (the others zero); vec: p is aligned for K elements
+    __device__ __forceinline__ void load(const IO *p, int n, bool vec) {
+        if (vec && n >= K) {
+            load(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+                const uint32_t b = i < n ? bits(p[i]) : 0;
+                if constexpr (sizeof(IO) == 4) w[i] = b;
+                else if (i % 2 == 0) w[i / 2] = b;
+                else w[i / 2] |= b << 16;
+            }
+        }
+    }
+    static __device__ __forceinline__ uint32_t bits(IO v) {
+        if constexpr (sizeof(IO) == 4) return __float_as_uint(v);
+        else return *reinterpret_cast<const uint16_t *>(&v);
+    }
+    __device__ __forceinline__ float2 pair(int i) const {  // elements i and i + 1, i even
+        if constexpr (sizeof(IO) == 4) {
+            return make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
+            return make_float2(__uint_as_float(w[i / 2] << 16), __uint_as_float(w[i / 2] & 0xffff0000u));
+        } else {
+            return __half22float2(*reinterpret_cast<const __half2 *>(&w[i / 2]));
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (K == 1) {
+            if constexpr (sizeof(IO) == 4) return __uint_as_float(w[0]);
+            const uint16_t h = (uint16_t)w[0];
+            return to_f32(*reinterpret_cast<const IO *>(&h));
+        }
+        const float2 v = pair(i & ~1);
+        return i & 1 ? v.y : v.x;
+    }
+    __device__ __forceinline__ void set_pair(int i, float x, float y) {
+        if constexpr (sizeof(IO) == 4) {
+            w[i] = __float_as_uint(x), w[i + 1] = __float_as_uint(y);
+        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(x, y);
+            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+};
+
+// Two fp32 fused multiply-adds in one instruction, each rounded like a scalar fmaf.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "mov.b64 pc, {%6, %7};\n\tfma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
 
 // Two values as e4m3 bytes (lo in the low byte), rounded to nearest even, saturating at 448; NaN -> 0x7f.
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {

@@ -260,6 +260,14 @@ SSD_API ssd_status_t ssd_conv(const ssd_conv_problem_t *prob, const ssd_conv_ten
     p.out_tok = t->out_tok;
     p.k = pr.width;
     p.silu = pr.activation == SSD_ACT_SILU;
+    p.rows = rows_seq;
+    const int64_t vec = 16 / (int64_t)es;
+    auto rows16 = [&](const void *q, int64_t seq, int64_t tok) {
+        return aligned(q, 16) && (rows_seq <= 1 || seq % vec == 0) && (pr.seqlen <= 1 || tok % vec == 0);
+    };
+    p.vec = pr.channels % vec == 0 && rows16(p.x, p.x_seq, p.x_tok) && rows16(p.out, p.out_seq, p.out_tok);
+    p.vec_state = aligned(p.state_out, 16) && aligned(p.state, 16);
+    p.vec_w = aligned(p.w, 16);
     return ssd::launch_row_conv(p, pr.io_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK
                                                                                                       : SSD_ERR_CUDA;
 }
@@ -306,6 +314,9 @@ SSD_API ssd_status_t ssd_group_norm(const ssd_norm_problem_t *prob, const ssd_no
     p.gate_first = pr.gate_first;
     p.silu = pr.activation == SSD_ACT_SILU;
     p.eps = pr.eps;
+    const int64_t vec = 16 / (int64_t)es, gs = pr.channels / pr.ngroups;  // 16-byte pieces of every group
+    p.vec = gs % vec == 0 && aligned(p.x, 16) && aligned(p.z, 16) && aligned(p.y, 16) && aligned(p.w, 16) &&
+            aligned(p.bias, 16) && (pr.rows == 1 || (p.x_row % vec == 0 && p.z_row % vec == 0 && p.y_row % vec == 0));
     return ssd::launch_norm(p, pr.io_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK
                                                                                                   : SSD_ERR_CUDA;
 }
@@ -332,6 +343,7 @@ SSD_API ssd_status_t ssd_fp8_quantize(int64_t rows, int64_t cols, int32_t block_
     p.cols = cols;
     p.x_row = x_row;
     p.block_rows = block_rows;
+    p.vec = aligned(x, 16) && aligned(q, 8) && cols % 8 == 0 && (rows == 1 || x_row * elem_size(io_dtype) % 16 == 0);
     return ssd::launch_quantize(p, io_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK
                                                                                                    : SSD_ERR_CUDA;
 }

@@ -27,8 +27,6 @@
 // axis, whatever their lengths; a segment restarts its chain wherever a sequence begins inside it.
 #pragma once
 
-#include <type_traits>
-
 #include "ssd_internal.h"
 #include "ssd_layer.cuh"
 
@@ -68,71 +66,6 @@ __device__ __forceinline__ void store_state(const ScanParams &p, void *s, int64_
     if (p.state_f16) *chk(static_cast<__half *>(s), i, 1, n, p.hdr, SITE_SCAN_STATE) = __float2half_rn(v);
     else *chk(static_cast<float *>(s), i, 1, n, p.hdr, SITE_SCAN_STATE) = v;
 }
-
-// K consecutive elements as they lie, in registers
-template <typename IO, int K> struct Raw {
-    static constexpr int W = K * (int)sizeof(IO) / 4;
-    uint32_t w[W];
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = 0;
-    }
-    // all K elements; p is aligned for them
-    __device__ __forceinline__ void load(const IO *p) {
-        if constexpr (W == 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            w[0] = v.x, w[1] = v.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < W / 4; ++i) {
-                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
-                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-            }
-        }
-    }
-    // the first n of K elements (the others zero); vec: p is aligned for K elements
-    __device__ __forceinline__ void load(const IO *p, int n, bool vec) {
-        if (vec && n >= K) {
-            load(p);
-        } else {
-#pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const uint32_t b = i < n ? bits(p[i]) : 0;
-                if constexpr (sizeof(IO) == 4) w[i] = b;
-                else if (i % 2 == 0) w[i / 2] = b;
-                else w[i / 2] |= b << 16;
-            }
-        }
-    }
-    static __device__ __forceinline__ uint32_t bits(IO v) {
-        if constexpr (sizeof(IO) == 4) return __float_as_uint(v);
-        else return *reinterpret_cast<const uint16_t *>(&v);
-    }
-    __device__ __forceinline__ float2 pair(int i) const {  // elements i and i + 1, i even
-        if constexpr (sizeof(IO) == 4) {
-            return make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
-            return make_float2(__uint_as_float(w[i / 2] << 16), __uint_as_float(w[i / 2] & 0xffff0000u));
-        } else {
-            return __half22float2(*reinterpret_cast<const __half2 *>(&w[i / 2]));
-        }
-    }
-    __device__ __forceinline__ float get(int i) const {
-        const float2 v = pair(i & ~1);
-        return i & 1 ? v.y : v.x;
-    }
-    __device__ __forceinline__ void set_pair(int i, float x, float y) {
-        if constexpr (sizeof(IO) == 4) {
-            w[i] = __float_as_uint(x), w[i + 1] = __float_as_uint(y);
-        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            const __half2 h = __floats2half2_rn(x, y);
-            w[i / 2] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-    }
-};
 
 // v[0 .. TG) of each of a channel's S lanes -> the total of item q TG / S, q the lane's place among them.
 template <int S, int TG> __device__ __forceinline__ float reduce_lanes(float (&v)[TG], int q) {
@@ -218,8 +151,9 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
     IO *raw = reinterpret_cast<IO *>(D_s + CT);                            // [2][x, dt, z][TT][CT]
     const int tid = threadIdx.x;
     const int64_t per_group = (p.cpg + CT - 1) / CT, ctiles = per_group * p.G;
-    const int64_t item = blockIdx.x / ctiles, ct = blockIdx.x % ctiles, g = ct / per_group;
-    const int64_t c0 = g * p.cpg + ct % per_group * CT;                    // first channel
+    int64_t ct, in_group;
+    const int64_t item = quick_div(blockIdx.x, ctiles, ct), g = quick_div(ct, per_group, in_group);
+    const int64_t c0 = g * p.cpg + in_group * CT;                          // first channel
     const int left = (int)((g + 1) * p.cpg - c0 < CT ? (g + 1) * p.cpg - c0 : CT);  // channels of this CTA
     const int ch = tid / S * kCH, q = tid % S;                             // this thread's first channel, its lane's place
     const int clive = left - ch < 0 ? 0 : left - ch < kCH ? left - ch : kCH;
@@ -255,8 +189,7 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
                         }
         }
     } else {
-        sq = item / nseg;
-        k = item % nseg;
+        sq = quick_div(item, nseg, k);
         t0 = k * p.seg_len;
         t1 = t0 + p.seg_len < p.L ? t0 + p.seg_len : p.L;
         fresh = k == 0;
@@ -593,9 +526,10 @@ __global__ void __launch_bounds__(256) step_kernel(ScanParams p) {
     constexpr int CT = 256 / S, TG = S < 8 ? S : 8;
     const int64_t ctiles = (p.D_ + CT - 1) / CT;
     const int ch = threadIdx.x / S, q = threadIdx.x % S, n0 = q * R;
-    const int64_t c = blockIdx.x % ctiles * CT + ch, s0 = blockIdx.x / ctiles * TG;
+    int64_t ct, rest;
+    const int64_t s0 = quick_div(blockIdx.x, ctiles, ct) * TG, c = ct * CT + ch;
     const bool live = c < p.D_;
-    const int64_t cc = live ? c : 0, cN = cc * p.N, g = cc / p.cpg;
+    const int64_t cc = live ? c : 0, cN = cc * p.N, g = quick_div(cc, p.cpg, rest);
     const int nl = live ? (int)(p.N - n0) : 0;  // states of this lane (may be negative)
     const int64_t total = p.nseq * p.D_ * p.N;
     (void)total;
