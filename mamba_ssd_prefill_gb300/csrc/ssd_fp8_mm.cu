@@ -544,7 +544,8 @@ cudaError_t launch_wide(const MatmulParams &p, int sms, cudaStream_t stream) {
     const int64_t tiles = ((p.m + 127) / 128) * ((p.n + 255) / 256);
     const size_t smem = kWS * kWStage + 8 * 4096 + 1024;
     auto k = wide_kernel<OUT>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k, smem, done);
     if (e != cudaSuccess) return e;
     const int vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_row * sizeof(OUT))) & 15) == 0;
     k<<<(unsigned)std::min<int64_t>(tiles, sms), kWThreads, smem, stream>>>(p, ma, mb, vec);
@@ -556,7 +557,8 @@ cudaError_t launch_narrow(const MatmulParams &p, int splits, cudaStream_t stream
     CUtensorMap mw, mt;
     if (!byte_map(&mw, p.b, p.n, p.k, 128) || !byte_map(&mt, p.a, p.m, p.k, TN)) return cudaErrorInvalidValue;
     auto k = narrow_kernel<OUT, TN>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Narrow<TN>::kDyn);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(k, Narrow<TN>::kDyn, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((p.n + 127) / 128 * splits), (unsigned)((p.m + TN - 1) / TN));

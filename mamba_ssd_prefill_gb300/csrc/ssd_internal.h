@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/ssd.h"
 #include "ssd_common.cuh"
@@ -74,6 +75,19 @@ cudaError_t launch_segstate(const Params &p, const SegPlan &sp, int io_dtype, in
 // ---- the operators around the SSD (ssd_layer_api.cu checks their arguments) ----
 
 int device_sms();  // SM count of the current device, 0 when it cannot be read (ssd_api.cu)
+
+// Lets `kernel` take `bytes` of dynamic shared memory on the current device; asked of the driver once per device
+// (`done`: a mask of the devices that have it, one per kernel).
+template <typename K> cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Packed or regular sequences of T tokens in all; strides in elements.
 struct ScanParams {

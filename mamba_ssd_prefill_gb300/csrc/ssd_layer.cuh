@@ -126,6 +126,11 @@ template <typename IO, int K> struct Raw {
     }
 };
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
 // Two fp32 fused multiply-adds in one instruction, each rounded like a scalar fmaf.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;

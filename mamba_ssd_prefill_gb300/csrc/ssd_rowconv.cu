@@ -66,11 +66,6 @@ __device__ __forceinline__ void next_sequence(const RowConvParams &p, Walk &w, i
     if (w.s >= p.nseq) w.s = p.nseq - 1, w.start = t, w.end = p.T + 1;  // malformed offsets
 }
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
-}
-
 // V channels a thread (16 bytes; V = 1: rows that are not 16-byte multiples). The rows come through a ring in shared
 // memory, kGroup tokens a stage, in slots that only their thread writes and reads (no barrier); V = 1 loads a stage's
 // tokens to registers instead.

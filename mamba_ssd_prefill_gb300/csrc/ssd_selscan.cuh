@@ -67,8 +67,9 @@ __device__ __forceinline__ void store_state(const ScanParams &p, void *s, int64_
     else *chk(static_cast<float *>(s), i, 1, n, p.hdr, SITE_SCAN_STATE) = v;
 }
 
-// v[0 .. TG) of each of a channel's S lanes -> the total of item q TG / S, q the lane's place among them.
-template <int S, int TG> __device__ __forceinline__ float reduce_lanes(float (&v)[TG], int q) {
+// v[0 .. TG), the shares of TG items in each of a channel's S lanes -> totals: lane q is left with the items q TG / S
+// onwards, TG / S of them (one where S >= TG) in v[0 ..].
+template <int S, int TG> __device__ __forceinline__ void reduce_lanes(float (&v)[TG], int q) {
     int m = TG;
 #pragma unroll
     for (int o = S / 2; o > 0; o /= 2) {
@@ -85,12 +86,6 @@ template <int S, int TG> __device__ __forceinline__ float reduce_lanes(float (&v
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
         }
     }
-    return v[0];
-}
-
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
 }
 
 // The last sequence whose start is at or before packed token t (empty ones before it share its start).
@@ -114,27 +109,6 @@ template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_ = 512 / NT_> stru
                2 * (size_t)TT * CT * es * (sum ? 2 : 3) + CT * 8;
     }
 };
-
-// v[c], the shares of a thread's CH channels in each of their S lanes -> totals: lane q is left with channels q CH / S
-// onwards, CH / S of them (one where S >= CH) in v[0 ..].
-template <int S, int CH> __device__ __forceinline__ void reduce_channels(float (&v)[CH], int q) {
-    int m = CH;
-#pragma unroll
-    for (int o = S / 2; o > 0; o /= 2) {
-        if (m > 1) {
-            m /= 2;
-            const bool upper = q & o;
-#pragma unroll
-            for (int i = 0; i < CH / 2; ++i)
-                if (i < m) {
-                    const float send = upper ? v[i] : v[i + m], keep = upper ? v[i + m] : v[i];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-        }
-    }
-}
 
 template <typename IO, typename T, bool SUM>
 __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
@@ -361,7 +335,7 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
                 if (SUM) part[c] += d[c];
             }
             if (!SUM) {
-                reduce_channels<S, kCH>(v, q);
+                reduce_lanes<S, kCH>(v, q);
                 constexpr int LEFT = S < kCH ? kCH / S : 1;  // channels left in this lane
                 const int c = ch + q * kCH / S;
                 float *o = ys + ys_at(t, c / 4) + c % 4;
@@ -518,115 +492,114 @@ static __global__ void __launch_bounds__(256) join_kernel(ScanParams p) {
     }
 }
 
-// One token for every sequence: the states are read and written once, from and to HBM, which bounds it. A thread keeps
-// the A of its R states for TG sequences, whose states are all in flight together; of a channel's S lanes each
-// discretises and gates for one of the sequences (as in the transposed sum above, which serves here too).
-template <typename IO, int S, int R>
-__global__ void __launch_bounds__(256) step_kernel(ScanParams p) {
-    constexpr int CT = 256 / S, TG = S < 8 ? S : 8;
+// One token for every sequence: the states are read and written once, from and to HBM, which bounds it. A thread takes
+// its R states of a channel through kSeqs sequences, whose states, B and C are all on their way before the first is used;
+// of a channel's S lanes each discretises and gates for some of the sequences (the sums over the lanes are transposed to
+// match), so that no softplus is taken twice.
+constexpr int kSeqs = 8;
+
+template <typename IO, typename ST, int S, int R>
+__global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
+    constexpr int CT = 128 / S, PER = kSeqs / S > 0 ? kSeqs / S : 1;  // channels of a CTA, sequences a lane gates for
     const int64_t ctiles = (p.D_ + CT - 1) / CT;
     const int ch = threadIdx.x / S, q = threadIdx.x % S, n0 = q * R;
     int64_t ct, rest;
-    const int64_t s0 = quick_div(blockIdx.x, ctiles, ct) * TG, c = ct * CT + ch;
+    const int64_t s0 = quick_div(blockIdx.x, ctiles, ct) * kSeqs, c = ct * CT + ch;
     const bool live = c < p.D_;
     const int64_t cc = live ? c : 0, cN = cc * p.N, g = quick_div(cc, p.cpg, rest);
     const int nl = live ? (int)(p.N - n0) : 0;  // states of this lane (may be negative)
-    const int64_t total = p.nseq * p.D_ * p.N;
+    const int ns = (int)(p.nseq - s0 < kSeqs ? p.nseq - s0 : kSeqs);
+    const int64_t total = p.nseq * p.D_ * p.N, seq_states = p.D_ * p.N;
     (void)total;
-    float h[TG][R], b[R], cs[R], a[R];
+    const bool whole = nl >= R;
+    Raw<ST, R> rh[kSeqs];
+    Raw<IO, R> rb[kSeqs], rc[kSeqs];
+    const ST *init = static_cast<const ST *>(p.init);
+    const IO *B = static_cast<const IO *>(p.B) + g * p.N + n0, *C = static_cast<const IO *>(p.C) + g * p.N + n0;
 #pragma unroll
-    for (int j = 0; j < TG; ++j) {
-        const int64_t i = (s0 + j) * p.D_ * p.N + cN + n0;
-        if (p.init && s0 + j < p.nseq && nl > 0) {
-            if (p.vec_state && nl >= R) {
-                if (p.state_f16) {
-                    Raw<__half, R> r;
-                    r.load(chk(static_cast<const __half *>(p.init), i, R, total, p.hdr, SITE_SCAN_STATE));
-#pragma unroll
-                    for (int k = 0; k < R; ++k) h[j][k] = r.get(k);
-                } else {
-                    Raw<float, R> r;
-                    r.load(chk(static_cast<const float *>(p.init), i, R, total, p.hdr, SITE_SCAN_STATE));
-#pragma unroll
-                    for (int k = 0; k < R; ++k) h[j][k] = r.get(k);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < R; ++k) h[j][k] = k < nl ? load_state(p, p.init, i + k) : 0.f;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < R; ++k) h[j][k] = 0.f;
+    for (int j = 0; j < kSeqs; ++j) {
+        rh[j].zero();
+        if (init && j < ns && nl > 0) {
+            const int64_t i = (s0 + j) * seq_states + cN + n0;
+            rh[j].load(chk(init, i, whole ? R : nl, total, p.hdr, SITE_SCAN_STATE), nl, p.vec_state);
         }
     }
+    // this lane's sequences of the group: mine, mine + 1, ..
+    const int mine = q * kSeqs / S;
+    float x[PER], d[PER], z[PER];
+    const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        x[j] = d[j] = z[j] = 0.f;
+        if (mine + j < ns) {
+            const int64_t s = s0 + mine + j;
+            x[j] = to_f32(static_cast<const IO *>(p.x)[s * p.x_seq + cc]);
+            d[j] = to_f32(static_cast<const IO *>(p.dt)[s * p.dt_seq + cc]) + bias;
+            if (p.z) z[j] = to_f32(static_cast<const IO *>(p.z)[s * p.z_seq + cc]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        rb[j].zero();
+        rc[j].zero();
+        if (j < ns && nl > 0) {
+            rb[j].load(B + (s0 + j) * p.b_seq, nl, p.vec_bc);
+            rc[j].load(C + (s0 + j) * p.c_seq, nl, p.vec_bc);
+        }
+    }
+    float a[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) a[k] = k < nl ? p.A[cN + n0 + k] * kLog2e : 0.f;
-    // lane q discretises for sequence mine (of the group of TG)
-    const int mine = q * TG / S;
-    float xv = 0.f, d = 0.f, zv = 0.f;
-    if (s0 + mine < p.nseq && live) {
-        const int64_t s = s0 + mine;
-        xv = to_f32(static_cast<const IO *>(p.x)[s * p.x_seq + cc]);
-        d = to_f32(static_cast<const IO *>(p.dt)[s * p.dt_seq + cc]) + (p.dt_bias ? p.dt_bias[cc] : 0.f);
-        if (p.z) zv = to_f32(static_cast<const IO *>(p.z)[s * p.z_seq + cc]);
-        if (p.softplus) d = softplus_fast(d);
+    float u[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (p.softplus) d[j] = softplus_fast(d[j]);
+        u[j] = d[j] * x[j];
     }
-    const float u = d * xv;
-    float v[TG];
+    float v[kSeqs];
+    ST *fin = static_cast<ST *>(p.fin);
 #pragma unroll
-    for (int j = 0; j < TG; ++j) {
-        const int src = j * (S / TG);
-        const float dj = __shfl_sync(0xffffffffu, d, src, S), uj = __shfl_sync(0xffffffffu, u, src, S);
-        float acc = 0.f;
-        if (s0 + j < p.nseq) {
-            const int64_t s = s0 + j;
-            const IO *B = static_cast<const IO *>(p.B) + s * p.b_seq + g * p.N + n0;
-            const IO *C = static_cast<const IO *>(p.C) + s * p.c_seq + g * p.N + n0;
-            if (p.vec_bc && nl >= R) {
-                Raw<IO, R> rb, rc;
-                rb.load(B);
-                rc.load(C);
+    for (int j = 0; j < kSeqs; ++j) {
+        const int src = j * S / kSeqs;  // the lane that discretised for sequence j
+        const float dj = __shfl_sync(0xffffffffu, d[j % PER], src, S), uj = __shfl_sync(0xffffffffu, u[j % PER], src, S);
+        float h[R], acc = 0.f;
 #pragma unroll
-                for (int k = 0; k < R; ++k) b[k] = rb.get(k), cs[k] = rc.get(k);
-            } else {
-#pragma unroll
-                for (int k = 0; k < R; ++k) b[k] = k < nl ? to_f32(B[k]) : 0.f, cs[k] = k < nl ? to_f32(C[k]) : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                h[j][k] = fmaf(ex2(dj * a[k]), h[j][k], uj * b[k]);
-                acc = fmaf(h[j][k], cs[k], acc);
-            }
-            if (p.fin && nl > 0) {
-                const int64_t i = s * p.D_ * p.N + cN + n0;
-                if (p.vec_state && nl >= R) {
-                    if (p.state_f16) {
-                        __half *o = chk(static_cast<__half *>(p.fin), i, R, total, p.hdr, SITE_SCAN_STATE);
-                        __half2 w[R / 2];
-#pragma unroll
-                        for (int k = 0; k < R / 2; ++k) w[k] = __floats2half2_rn(h[j][2 * k], h[j][2 * k + 1]);
-                        if constexpr (R == 4) *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(w);
-                        else *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(w);
-                    } else {
-                        float *o = chk(static_cast<float *>(p.fin), i, R, total, p.hdr, SITE_SCAN_STATE);
-#pragma unroll
-                        for (int k = 0; k < R; k += 4)
-                            *reinterpret_cast<float4 *>(o + k) = make_float4(h[j][k], h[j][k + 1], h[j][k + 2], h[j][k + 3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < R; ++k)
-                        if (k < nl) store_state(p, p.fin, i + k, h[j][k]);
-                }
-            }
+        for (int k = 0; k < R; ++k) {
+            h[k] = fmaf(ex2(dj * a[k]), rh[j].get(k), uj * rb[j].get(k));
+            acc = fmaf(h[k], rc[j].get(k), acc);
         }
         v[j] = acc;
+        if (fin && j < ns && nl > 0) {
+            ST *o = chk(fin, (s0 + j) * seq_states + cN + n0, whole ? R : nl, total, p.hdr, SITE_SCAN_STATE);
+            if (p.vec_state && whole) {
+                Raw<ST, R> w;
+#pragma unroll
+                for (int k = 0; k < R; k += 2) w.set_pair(k, h[k], h[k + 1]);
+                if constexpr (Raw<ST, R>::W == 2) {
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(w.w[0], w.w[1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < Raw<ST, R>::W; k += 4)
+                        reinterpret_cast<uint4 *>(o)[k / 4] = make_uint4(w.w[k], w.w[k + 1], w.w[k + 2], w.w[k + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < R; ++k)
+                    if (k < nl) o[k] = from_f32<ST>(h[k]);
+            }
+        }
     }
-    float y = fmaf(p.D ? p.D[cc] : 0.f, xv, reduce_lanes<S, TG>(v, q));
-    if (p.z) y *= silu_f32(zv);
-    if (live && s0 + mine < p.nseq && (S <= TG || q % (S / TG) == 0))
-        *chk(static_cast<IO *>(p.y), (s0 + mine) * p.y_seq + cc, 1, (p.rows - 1) * p.y_seq + p.D_, p.hdr,
-             SITE_SCAN_Y) = from_f32<IO>(y);
+    reduce_lanes<S, kSeqs>(v, q);
+    const float Dc = p.D ? p.D[cc] : 0.f;
+    if (live && (S <= kSeqs || q % (S / kSeqs) == 0))
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (mine + j < ns) {
+                float y = fmaf(Dc, x[j], v[j]);
+                if (p.z) y *= silu_f32(z[j]);
+                *chk(static_cast<IO *>(p.y), (s0 + mine + j) * p.y_seq + cc, 1, (p.rows - 1) * p.y_seq + p.D_, p.hdr,
+                     SITE_SCAN_Y) = from_f32<IO>(y);
+            }
 }
 
 template <typename IO, typename T, bool SUM>
@@ -636,7 +609,8 @@ cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream)
     auto k = scan_kernel<IO, T, SUM>;
     constexpr size_t smem = T::smem(SUM, sizeof(IO));
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(k, smem, done);
         if (e != cudaSuccess) return e;
     }
     k<<<(unsigned)grid, T::NT, smem, stream>>>(p);
@@ -659,10 +633,11 @@ cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
 }
 template <typename IO, int S, int R>
 cudaError_t launch_step_kernel(const ScanParams &p, cudaStream_t stream) {
-    constexpr int CT = 256 / S, TG = S < 8 ? S : 8;
-    const int64_t grid = (p.D_ + CT - 1) / CT * ((p.nseq + TG - 1) / TG);
+    constexpr int CT = 128 / S;
+    const int64_t grid = (p.D_ + CT - 1) / CT * ((p.nseq + kSeqs - 1) / kSeqs);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    step_kernel<IO, S, R><<<(unsigned)grid, 256, 0, stream>>>(p);
+    if (p.state_f16) step_kernel<IO, __half, S, R><<<(unsigned)grid, 128, 0, stream>>>(p);
+    else step_kernel<IO, float, S, R><<<(unsigned)grid, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -13,6 +13,8 @@ import struct
 
 import torch
 
+import mamba_ssd_prefill_gb300 as _m
+
 _F32, _I32 = torch.float32, torch.int32
 _IO = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _STATE = {torch.float32: 0, torch.float16: 2}
@@ -29,56 +31,63 @@ _NORM_TENSORS = struct.Struct("@6P3q").pack
 _MATMUL_PROBLEM = struct.Struct("@3q2i").pack
 
 
-class _Call:
-    """Device, stream and workspace of one call."""
+_empty = torch.empty
+_workspaces: dict = {}  # (use, device, stream) -> (tensor, address, bytes)
 
-    __slots__ = ("device", "stream", "raw", "side", "ws", "guard")
 
-    def __init__(self, device, stream, workspace, kind, nbytes=256):
-        import mamba_ssd_prefill_gb300 as m
+def _raw_stream(index):
+    """Address of the device's current stream (0: the default one)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
-        self.device = device
-        current = torch.cuda.current_stream(device)
-        self.side = stream is not None and stream != current
-        self.stream = stream if self.side else current
-        self.raw = self.stream.cuda_stream
-        self.guard = torch.cuda.current_device() != device.index
-        if workspace is None:
-            key = (kind, device.index, self.raw)
-            workspace = m._default_ws.get(key)
-            if workspace is None:
-                workspace = m._default_ws.setdefault(key, m.Workspace(device))
-        if isinstance(workspace, m.Workspace):
-            self.ws = self.on(lambda: workspace.get(nbytes))
-        else:
-            self.ws = workspace
 
-    def on(self, make):
-        """make() with the call's stream current, so that what it allocates belongs to that stream."""
-        if not self.side:
-            return make()
-        with torch.cuda.stream(self.stream):
-            return make()
+def _enter(dev, stream, workspace, use, nbytes=256):
+    """(stream address, stream if it is not the current one, workspace address, its bytes, the tensor behind it)."""
+    index = dev.index
+    raw, side = _raw_stream(index), None
+    if stream is not None and stream.cuda_stream != raw:
+        raw, side = stream.cuda_stream, stream
+    if workspace is None:
+        key = (use, index, raw)
+        have = _workspaces.get(key)
+        if have is None or have[2] < nbytes:
+            buf = _on(side, lambda: torch.zeros(nbytes, dtype=torch.uint8, device=dev))
+            have = _workspaces[key] = (buf, buf.data_ptr(), nbytes)
+        return raw, side, have[1], have[2], have[0]
+    if isinstance(workspace, _m.Workspace):
+        workspace = _on(side, lambda: workspace.get(nbytes))
+    return raw, side, workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
-    def empty(self, shape, dtype):
-        if not self.side:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        return self.on(lambda: torch.empty(shape, dtype=dtype, device=self.device))
 
-    def run(self, what, fn, *args, used=()):
-        import mamba_ssd_prefill_gb300 as m
+def _on(side, make):
+    """make() with stream `side` current (None: as it is), so that what it allocates belongs to that stream."""
+    if side is None:
+        return make()
+    with torch.cuda.stream(side):
+        return make()
 
-        if self.guard:
-            with torch.cuda.device(self.device):
-                st = fn(*args, self.raw)
-        else:
-            st = fn(*args, self.raw)
-        if st:
-            raise m.SsdError(st, what)
-        if self.side:  # memory of other streams: not reused before this stream is done with it
-            for t in used:
-                if t is not None:
-                    t.record_stream(self.stream)
+
+def _new(side, shape, dtype, dev):
+    if side is None:
+        return _empty(shape, dtype=dtype, device=dev)
+    return _on(side, lambda: _empty(shape, dtype=dtype, device=dev))
+
+
+def _call(what, fn, dev, *args):
+    """fn(*args) on the tensors' device; raises SsdError."""
+    if torch._C._cuda_getDevice() != dev.index:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    else:
+        st = fn(*args)
+    if st:
+        raise _m.SsdError(st, what)
+
+
+def _keep(side, *used):
+    """Memory of other streams is not reused before the work on stream `side` is done with it."""
+    for t in used:
+        if t is not None:
+            t.record_stream(side)
 
 
 def _ptr(t):
@@ -91,12 +100,6 @@ def _device(what, t):
     return t.device
 
 
-def _lib():
-    import mamba_ssd_prefill_gb300 as m
-
-    return m.lib()
-
-
 def _check(name, t, shape, dtype, dev):
     """t has this shape, type and device and contiguous rows (the last dimension)."""
     if t.shape != shape or t.dtype is not dtype or t.device != dev or (t.stride(-1) != 1 and shape[-1] > 1):
@@ -106,7 +109,9 @@ def _check(name, t, shape, dtype, dev):
 
 def _flat(name, t, shape, dtype, dev):
     """t has this shape, type and device and is contiguous."""
-    if t is not None and (t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous()):
+    if t is None:
+        return
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 
@@ -138,60 +143,66 @@ def ssd_selective_scan(x, dt_raw, dt_bias, A, B, C, D=None, z=None, init_states=
     [nseq, Dc, N]. final_states may be init_states itself (a cache advanced in place). Returns (y, final_states or
     None). Malformed offsets are reported by check() on the workspace."""
     nseq, dev = _sequences("ssd_selective_scan", x, cu_seqlens)
-    b, L, Dc = x.shape
-    io = x.dtype
-    if io not in _IO:
-        raise ValueError(f"x: unsupported dtype {io}")
+    shape, io = x.shape, x.dtype
+    b, L, Dc = shape
     if B.dim() != 4:
         raise ValueError("B: expected [batch, seqlen, ngroups, dstate]")
-    G, N = B.shape[2], B.shape[3]
+    G, N = B.shape[2:]
     if state_dtype is None:
         state_dtype = init_states.dtype if init_states is not None else _F32
+    if io not in _IO:
+        raise ValueError(f"x: unsupported dtype {io}")
     if state_dtype not in _STATE:
         raise ValueError(f"state_dtype: expected fp32 or fp16, got {state_dtype}")
     if Dc < 1 or N < 1 or G < 1 or Dc % G:
         raise ValueError(f"channels {Dc} must be a positive multiple of the {G} groups, with at least one state")
-    shape = (b, L, Dc)
-    _check("x", x, shape, io, dev)
-    _check("dt_raw", dt_raw, shape, io, dev)
-    for name, t in (("B", B), ("C", C)):
-        _check(name, t, (b, L, G, N), io, dev)
-        if G > 1 and t.stride(2) != N:
-            raise ValueError(f"{name}: a token's [ngroups, dstate] must be contiguous")
-    _flat("A", A, (Dc, N), _F32, dev)
-    _flat("dt_bias", dt_bias, (Dc,), _F32, dev)
-    _flat("D", D, (Dc,), _F32, dev)
+    xs, ds, bs, cs = x.stride(), dt_raw.stride(), B.stride(), C.stride()
+    if (dt_raw.shape != shape or dt_raw.dtype is not io or dt_raw.device != dev or xs[2] != 1 or ds[2] != 1
+            or B.shape[:2] != shape[:2] or B.dtype is not io or B.device != dev or bs[3] != 1
+            or C.shape != B.shape or C.dtype is not io or C.device != dev or cs[3] != 1
+            or (G > 1 and (bs[2] != N or cs[2] != N))
+            or A.shape != (Dc, N) or A.dtype is not _F32 or A.device != dev or not A.is_contiguous()):
+        _check("x", x, shape, io, dev)
+        _check("dt_raw", dt_raw, shape, io, dev)
+        for name, t in (("B", B), ("C", C)):
+            _check(name, t, (b, L, G, N), io, dev)
+            if G > 1 and t.stride(2) != N:
+                raise ValueError(f"{name}: a token's [ngroups, dstate] must be contiguous")
+        _flat("A", A, (Dc, N), _F32, dev)
+    for name, t in (("dt_bias", dt_bias), ("D", D)):
+        if t is not None and (t.shape != (Dc,) or t.dtype is not _F32 or t.device != dev or not t.is_contiguous()):
+            _flat(name, t, (Dc,), _F32, dev)
+    zs = (0, 0)
+    if z is not None:
+        zs = z.stride()
+        if z.shape != shape or z.dtype is not io or z.device != dev or zs[2] != 1:
+            _check("z", z, shape, io, dev)
     _flat("init_states", init_states, (nseq, Dc, N), state_dtype, dev)
     _flat("final_states", final_states, (nseq, Dc, N), state_dtype, dev)
-    L_ = _lib()
+    lib = _m.lib()
     prob = _SCAN_PROBLEM(nseq, L, Dc, N, G, _IO[io], _STATE[state_dtype], cu_seqlens is not None, bool(softplus))
-    n = ctypes.c_size_t(0)
-    st = L_.ssd_selective_scan_workspace_size(prob, ctypes.byref(n))
-    if st:
-        import mamba_ssd_prefill_gb300 as m
-
-        raise m.SsdError(st, "ssd_selective_scan")
-    call = _Call(dev, stream, workspace, "scan", n.value)
+    nbytes = 256
+    if L != 1:  # a single token needs the header only
+        n = ctypes.c_size_t(0)
+        st = lib.ssd_selective_scan_workspace_size(prob, ctypes.byref(n))
+        if st:
+            raise _m.SsdError(st, "ssd_selective_scan")
+        nbytes = n.value
+    raw, side, ws, ws_bytes, ws_buf = _enter(dev, stream, workspace, "scan", nbytes)
     if y is None:
-        y = call.empty(shape, io)
+        y = _new(side, shape, io, dev)
     else:
         _check("y", y, shape, io, dev)
     if final_states is None and return_final_states:
-        final_states = call.empty((nseq, Dc, N), state_dtype)
-    xs, ds, bs, cs, ys = x.stride(), dt_raw.stride(), B.stride(), C.stride(), y.stride()
-    if z is not None:
-        _check("z", z, shape, io, dev)
-        zs = z.stride()
-    else:
-        zs = (0, 0)
+        final_states = _new(side, (nseq, Dc, N), state_dtype, dev)
+    ys = y.stride()
     tensors = _SCAN_TENSORS(x.data_ptr(), dt_raw.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), y.data_ptr(),
                             A.data_ptr(), _ptr(dt_bias), _ptr(D), _ptr(init_states), _ptr(final_states),
                             _ptr(cu_seqlens), xs[0], xs[1], ds[0], ds[1], zs[0], zs[1], bs[0], bs[1], cs[0], cs[1],
                             ys[0], ys[1])
-    ws = call.ws
-    call.run("ssd_selective_scan", L_.ssd_selective_scan, prob, tensors, ws.data_ptr(),
-             ws.numel() * ws.element_size(),
-             used=(x, dt_raw, dt_bias, A, B, C, D, z, init_states, cu_seqlens, y, final_states, ws))
+    _call("ssd_selective_scan", lib.ssd_selective_scan, dev, prob, tensors, ws, ws_bytes, raw)
+    if side is not None:
+        _keep(side, x, dt_raw, dt_bias, A, B, C, D, z, init_states, cu_seqlens, y, final_states, ws_buf)
     return y, final_states
 
 
@@ -220,24 +231,27 @@ def ssd_conv(x, conv_weight, conv_bias=None, conv_state=None, cu_seqlens=None, a
     _flat("conv_bias", conv_bias, (Dc,), _F32, dev)
     _flat("conv_state", conv_state, (nseq, Dc, k - 1), io, dev)
     _flat("conv_state_out", conv_state_out, (nseq, Dc, k - 1), io, dev)
-    call = _Call(dev, stream, workspace, "conv")
+    raw, side, ws, _, ws_buf = _enter(dev, stream, workspace, "conv")
     if out is None:
-        out = call.empty(shape, io)
+        out = _new(side, shape, io, dev)
     else:
         _check("out", out, shape, io, dev)
     if conv_state_out is None and return_conv_state:
-        conv_state_out = call.empty((nseq, Dc, k - 1), io)
+        conv_state_out = _new(side, (nseq, Dc, k - 1), io, dev)
     xs, os = x.stride(), out.stride()
     prob = _CONV_PROBLEM(nseq, L, Dc, k, _ACT[activation], _IO[io], cu_seqlens is not None)
     tensors = _CONV_TENSORS(x.data_ptr(), out.data_ptr(), conv_weight.data_ptr(), _ptr(conv_bias), _ptr(conv_state),
                             _ptr(conv_state_out), _ptr(cu_seqlens), xs[0], xs[1], os[0], os[1])
-    call.run("ssd_conv", _lib().ssd_conv, prob, tensors, call.ws.data_ptr(),
-             used=(x, conv_weight, conv_bias, conv_state, cu_seqlens, out, conv_state_out, call.ws))
+    _call("ssd_conv", _m.lib().ssd_conv, dev, prob, tensors, ws, raw)
+    if side is not None:
+        _keep(side, x, conv_weight, conv_bias, conv_state, cu_seqlens, out, conv_state_out, ws_buf)
     return out, conv_state_out
 
 
 def _rows(name, t, dtype, dev, shape):
     """t [..., channels] as evenly spaced rows: the row stride."""
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return shape[-1]
     _check(name, t, shape, dtype, dev)
     if t.dim() == 1 or t.is_contiguous():
         return shape[-1]
@@ -272,21 +286,22 @@ def ssd_group_norm(x, weight=None, bias=None, z=None, ngroups=1, eps=1e-5, *, ce
     z_row = _rows("z", z, io, dev, shape) if z is not None else 0
     _flat("weight", weight, (Dc,), _F32, dev)
     _flat("bias", bias, (Dc,), _F32, dev)
-    call = _Call(dev, stream, workspace, "norm")
+    raw, side, ws, _, ws_buf = _enter(dev, stream, workspace, "norm")
     scales = None
     if y is None:
-        y = call.empty(shape, E4M3 if quantize else io)
+        y = _new(side, shape, E4M3 if quantize else io, dev)
         y_row = Dc
     else:
         y_row = _rows("y", y, E4M3 if quantize else io, dev, shape)
     if quantize:
-        scales = call.empty((*shape[:-1], -(-Dc // 128)), _F32)
+        scales = _new(side, (*shape[:-1], -(-Dc // 128)), _F32, dev)
     prob = _NORM_PROBLEM(x.numel() // Dc, Dc, ngroups, _IO[io], _ACT[activation], bool(center), bool(gate_first),
                          eps, 0)
     tensors = _NORM_TENSORS(x.data_ptr(), _ptr(z), y.data_ptr(), _ptr(scales), _ptr(weight), _ptr(bias), x_row,
                             z_row, y_row)
-    call.run("ssd_group_norm", _lib().ssd_group_norm, prob, tensors, call.ws.data_ptr(),
-             used=(x, z, weight, bias, y, scales, call.ws))
+    _call("ssd_group_norm", _m.lib().ssd_group_norm, dev, prob, tensors, ws, raw)
+    if side is not None:
+        _keep(side, x, z, weight, bias, y, scales, ws_buf)
     return (y, scales) if quantize else y
 
 
@@ -306,11 +321,14 @@ def ssd_fp8_quantize(x, block_rows=1, *, workspace=None, stream=None):
     K = shape[-1]
     x_row = _rows("x", x, io, dev, shape)
     rows = x.numel() // K if K else 0
-    call = _Call(dev, stream, workspace, "fp8")
-    q = call.empty(shape, E4M3)
-    scales = call.empty((*shape[:-1], -(-K // 128)) if block_rows == 1 else (-(-rows // 128), -(-K // 128)), _F32)
-    call.run("ssd_fp8_quantize", _lib().ssd_fp8_quantize, rows, K, block_rows, _IO[io], x.data_ptr(), x_row,
-             q.data_ptr(), scales.data_ptr(), call.ws.data_ptr(), used=(x, q, scales, call.ws))
+    raw, side, ws, _, ws_buf = _enter(dev, stream, workspace, "fp8")
+    q = _new(side, shape, E4M3, dev)
+    kb = -(-K // 128)
+    scales = _new(side, (*shape[:-1], kb) if block_rows == 1 else (-(-rows // 128), kb), _F32, dev)
+    _call("ssd_fp8_quantize", _m.lib().ssd_fp8_quantize, dev, rows, K, block_rows, _IO[io], x.data_ptr(), x_row,
+          q.data_ptr(), scales.data_ptr(), ws, raw)
+    if side is not None:
+        _keep(side, x, q, scales, ws_buf)
     return q, scales
 
 
@@ -334,15 +352,15 @@ def ssd_fp8_matmul(a, a_scales, b, b_scales, bias=None, *, out_dtype=torch.bfloa
     _flat("b_scales", b_scales, (-(-N // 128), kb), _F32, dev)
     _flat("bias", bias, (N,), _F32, dev)
     M = lead.numel()
-    call = _Call(dev, stream, workspace, "fp8")
+    raw, side, ws, ws_bytes, ws_buf = _enter(dev, stream, workspace, "fp8")
     if out is None:
-        out = call.empty((*lead, N), out_dtype)
+        out = _new(side, (*lead, N), out_dtype, dev)
         out_row = N
     else:
         out_row = _rows("out", out, out_dtype, dev, (*lead, N))
-    ws = call.ws
-    call.run("ssd_fp8_matmul", _lib().ssd_fp8_matmul, _MATMUL_PROBLEM(M, N, K, _IO[out_dtype], 0), a.data_ptr(),
-             a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), _ptr(bias), out.data_ptr(), out_row,
-             ws.data_ptr(), ws.numel() * ws.element_size(),
-             used=(a, a_scales, b, b_scales, bias, out, ws))
+    _call("ssd_fp8_matmul", _m.lib().ssd_fp8_matmul, dev, _MATMUL_PROBLEM(M, N, K, _IO[out_dtype], 0), a.data_ptr(),
+          a_scales.data_ptr(), b.data_ptr(), b_scales.data_ptr(), _ptr(bias), out.data_ptr(), out_row, ws, ws_bytes,
+          raw)
+    if side is not None:
+        _keep(side, a, a_scales, b, b_scales, bias, out, ws_buf)
     return out
