@@ -512,94 +512,126 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
     const int64_t total = p.nseq * p.D_ * p.N, seq_states = p.D_ * p.N;
     (void)total;
     const bool whole = nl >= R;
-    Raw<ST, R> rh[kSeqs];
-    Raw<IO, R> rb[kSeqs], rc[kSeqs];
-    const ST *init = static_cast<const ST *>(p.init);
-    const IO *B = static_cast<const IO *>(p.B) + g * p.N + n0, *C = static_cast<const IO *>(p.C) + g * p.N + n0;
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        rh[j].zero();
-        if (init && j < ns && nl > 0) {
-            const int64_t i = (s0 + j) * seq_states + cN + n0;
-            rh[j].load(chk(init, i, whole ? R : nl, total, p.hdr, SITE_SCAN_STATE), nl, p.vec_state);
-        }
-    }
-    // this lane's sequences of the group: mine, mine + 1, ..
-    const int mine = q * kSeqs / S;
-    float x[PER], d[PER], z[PER];
-    const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        x[j] = d[j] = z[j] = 0.f;
-        if (mine + j < ns) {
-            const int64_t s = s0 + mine + j;
-            x[j] = to_f32(static_cast<const IO *>(p.x)[s * p.x_seq + cc]);
-            d[j] = to_f32(static_cast<const IO *>(p.dt)[s * p.dt_seq + cc]) + bias;
-            if (p.z) z[j] = to_f32(static_cast<const IO *>(p.z)[s * p.z_seq + cc]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        rb[j].zero();
-        rc[j].zero();
-        if (j < ns && nl > 0) {
-            rb[j].load(B + (s0 + j) * p.b_seq, nl, p.vec_bc);
-            rc[j].load(C + (s0 + j) * p.c_seq, nl, p.vec_bc);
-        }
-    }
+    const int mine = q * kSeqs / S;  // this lane discretises and gates for the sequences mine, mine + 1, ..
+    const int64_t i0 = s0 * seq_states + cN + n0;
+    const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, Dc = p.D ? p.D[cc] : 0.f;
     float a[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) a[k] = k < nl ? p.A[cN + n0 + k] * kLog2e : 0.f;
-    float u[PER];
+
+    // FAST: all of the group's sequences and of this lane's states exist, and whole vectors are aligned
+    auto body = [&](auto fast) {
+        constexpr bool FAST = decltype(fast)::value;
+        Raw<ST, R> rh[kSeqs];
+        Raw<IO, R> rb[kSeqs], rc[kSeqs];
+        const ST *init = static_cast<const ST *>(p.init);
+        if (init) {
+            const ST *hp = chk(init, i0, FAST ? R : nl < 0 ? 0 : nl < R ? nl : R, total, p.hdr, SITE_SCAN_STATE);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        if (p.softplus) d[j] = softplus_fast(d[j]);
-        u[j] = d[j] * x[j];
-    }
-    float v[kSeqs];
-    ST *fin = static_cast<ST *>(p.fin);
+            for (int j = 0; j < kSeqs; ++j) {
+                if constexpr (FAST) {
+                    rh[j].load(hp + j * seq_states);
+                } else {
+                    rh[j].zero();
+                    if (j < ns && nl > 0) rh[j].load(hp + j * seq_states, nl, p.vec_state);
+                }
+            }
+        } else {
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int src = j * S / kSeqs;  // the lane that discretised for sequence j
-        const float dj = __shfl_sync(0xffffffffu, d[j % PER], src, S), uj = __shfl_sync(0xffffffffu, u[j % PER], src, S);
-        float h[R], acc = 0.f;
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            h[k] = fmaf(ex2(dj * a[k]), rh[j].get(k), uj * rb[j].get(k));
-            acc = fmaf(h[k], rc[j].get(k), acc);
+            for (int j = 0; j < kSeqs; ++j) rh[j].zero();
         }
-        v[j] = acc;
-        if (fin && j < ns && nl > 0) {
-            ST *o = chk(fin, (s0 + j) * seq_states + cN + n0, whole ? R : nl, total, p.hdr, SITE_SCAN_STATE);
-            if (p.vec_state && whole) {
-                Raw<ST, R> w;
+        float x[PER], d[PER], z[PER], u[PER];
+        {
+            const IO *xp = static_cast<const IO *>(p.x) + (s0 + mine) * p.x_seq + cc;
+            const IO *dp = static_cast<const IO *>(p.dt) + (s0 + mine) * p.dt_seq + cc;
+            const IO *zp = p.z ? static_cast<const IO *>(p.z) + (s0 + mine) * p.z_seq + cc : nullptr;
 #pragma unroll
-                for (int k = 0; k < R; k += 2) w.set_pair(k, h[k], h[k + 1]);
-                if constexpr (Raw<ST, R>::W == 2) {
-                    *reinterpret_cast<uint2 *>(o) = make_uint2(w.w[0], w.w[1]);
+            for (int j = 0; j < PER; ++j) {
+                x[j] = d[j] = z[j] = 0.f;
+                if (FAST || mine + j < ns) {
+                    x[j] = to_f32(xp[j * p.x_seq]);
+                    d[j] = to_f32(dp[j * p.dt_seq]) + bias;
+                    if (zp) z[j] = to_f32(zp[j * p.z_seq]);
+                }
+            }
+        }
+        {
+            const IO *B = static_cast<const IO *>(p.B) + s0 * p.b_seq + g * p.N + n0;
+            const IO *C = static_cast<const IO *>(p.C) + s0 * p.c_seq + g * p.N + n0;
+#pragma unroll
+            for (int j = 0; j < kSeqs; ++j) {
+                if constexpr (FAST) {
+                    rb[j].load(B + j * p.b_seq);
+                    rc[j].load(C + j * p.c_seq);
+                } else {
+                    rb[j].zero();
+                    rc[j].zero();
+                    if (j < ns && nl > 0) {
+                        rb[j].load(B + j * p.b_seq, nl, p.vec_bc);
+                        rc[j].load(C + j * p.c_seq, nl, p.vec_bc);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            if (p.softplus) d[j] = softplus_fast(d[j]);
+            u[j] = d[j] * x[j];
+        }
+        float v[kSeqs];
+        ST *fp = static_cast<ST *>(p.fin);
+        if (fp) fp = chk(fp, i0, FAST ? R : nl < 0 ? 0 : nl < R ? nl : R, total, p.hdr, SITE_SCAN_STATE);
+#pragma unroll
+        for (int j = 0; j < kSeqs; ++j) {
+            const int src = j * S / kSeqs;  // the lane that discretised for sequence j
+            const float dj = __shfl_sync(0xffffffffu, d[j % PER], src, S);
+            const float uj = __shfl_sync(0xffffffffu, u[j % PER], src, S);
+            float h[R], acc = 0.f;
+#pragma unroll
+            for (int k = 0; k < R; k += 2) {
+                const float2 h2 = rh[j].pair(k), b2 = rb[j].pair(k), c2 = rc[j].pair(k);
+                h[k] = fmaf(ex2(dj * a[k]), h2.x, uj * b2.x);
+                h[k + 1] = fmaf(ex2(dj * a[k + 1]), h2.y, uj * b2.y);
+                acc = fmaf(h[k + 1], c2.y, fmaf(h[k], c2.x, acc));
+            }
+            v[j] = acc;
+            if (fp && (FAST || (j < ns && nl > 0))) {
+                ST *o = fp + j * seq_states;
+                if (FAST || (p.vec_state && whole)) {
+                    Raw<ST, R> w;
+#pragma unroll
+                    for (int k = 0; k < R; k += 2) w.set_pair(k, h[k], h[k + 1]);
+                    if constexpr (Raw<ST, R>::W == 2) {
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(w.w[0], w.w[1]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < Raw<ST, R>::W; k += 4)
+                            reinterpret_cast<uint4 *>(o)[k / 4] =
+                                make_uint4(w.w[k], w.w[k + 1], w.w[k + 2], w.w[k + 3]);
+                    }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < Raw<ST, R>::W; k += 4)
-                        reinterpret_cast<uint4 *>(o)[k / 4] = make_uint4(w.w[k], w.w[k + 1], w.w[k + 2], w.w[k + 3]);
+                    for (int k = 0; k < R; ++k)
+                        if (k < nl) o[k] = from_f32<ST>(h[k]);
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < R; ++k)
-                    if (k < nl) o[k] = from_f32<ST>(h[k]);
             }
         }
-    }
-    reduce_lanes<S, kSeqs>(v, q);
-    const float Dc = p.D ? p.D[cc] : 0.f;
-    if (live && (S <= kSeqs || q % (S / kSeqs) == 0))
+        reduce_lanes<S, kSeqs>(v, q);
+        if (live && (S <= kSeqs || q % (S / kSeqs) == 0))
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (mine + j < ns) {
-                float y = fmaf(Dc, x[j], v[j]);
-                if (p.z) y *= silu_f32(z[j]);
-                *chk(static_cast<IO *>(p.y), (s0 + mine + j) * p.y_seq + cc, 1, (p.rows - 1) * p.y_seq + p.D_, p.hdr,
-                     SITE_SCAN_Y) = from_f32<IO>(y);
-            }
+            for (int j = 0; j < PER; ++j)
+                if (FAST || mine + j < ns) {
+                    float y = fmaf(Dc, x[j], v[j]);
+                    if (p.z) y *= silu_f32(z[j]);
+                    *chk(static_cast<IO *>(p.y), (s0 + mine + j) * p.y_seq + cc, 1, (p.rows - 1) * p.y_seq + p.D_, p.hdr,
+                         SITE_SCAN_Y) = from_f32<IO>(y);
+                }
+    };
+    // the same for all lanes of a warp, which exchange values inside
+    if (__all_sync(0xffffffffu, ns == kSeqs && live && whole && p.vec_state && p.vec_bc))
+        body(std::integral_constant<bool, true>());
+    else
+        body(std::integral_constant<bool, false>());
 }
 
 template <typename IO, typename T, bool SUM>
