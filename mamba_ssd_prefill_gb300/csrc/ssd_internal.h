@@ -108,16 +108,18 @@ struct ScanParams {
     int64_t nseg, seg_len, seg_items;
     float *seg_state, *seg_dt;
 };
-// Channels and threads of a scan CTA, by the number of states (the shapes in ssd_selscan.cuh).
+// Channels and threads of a scan CTA, and the threads that an SM holds, by the number of states (the shapes in
+// ssd_selscan.cuh).
 struct ScanCta {
-    int channels, threads;
+    int channels, threads, resident;
 };
 inline ScanCta scan_cta(int64_t N) {
-    if (N <= 4) return {128, 32};
-    if (N <= 8) return {128, 64};
-    if (N <= 24) return {128, 128};
-    if (N <= 32) return {128, 256};
-    return {N <= 64 ? 64 : N <= 128 ? 32 : 16, 256};
+    if (N <= 4) return {128, 32, 512};
+    if (N <= 8) return {128, 64, 640};
+    if (N <= 16) return {128, 128, 640};
+    if (N <= 24) return {128, 128, 512};
+    if (N <= 32) return {128, 256, 512};
+    return {N <= 64 ? 64 : N <= 128 ? 32 : 16, 256, 512};
 }
 // ssd_selscan.cuh, one translation unit per type
 cudaError_t launch_scan_f32(const ScanParams &p, cudaStream_t stream);

@@ -59,12 +59,12 @@ ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments) {
     // Without segments the work of a chain runs once, with them its states' part twice. So segments are cut only where
     // the CTAs leave the SMs short of warps (under about 1.3 CTAs of 128 threads each: 4 x 4096 x 1536 x 16, 48 CTAs,
     // 0.84 ms in one chain and 0.24 segmented; 32 x 4096 x 1536 x 16, 384 CTAs, 1.28 and 1.57 ms), and then so many that
-    // two waves of resident CTAs (640 threads an SM) fill: fewer leave a ragged wave, more pay the entry of a segment.
+    // two waves of resident CTAs fill: fewer leave a ragged wave, more pay the entry of a segment.
     const ssd::ScanCta cta = ssd::scan_cta(p.dstate);
     const int64_t per_group = (p.channels / p.ngroups + cta.channels - 1) / cta.channels;
     const int64_t ctas = chains * p.ngroups * per_group, threads = ctas * cta.threads;
     if (threads * 10 >= 13 * 128 * (int64_t)sms) return pl;
-    const int64_t want = std::min<int64_t>(2 * 640 * (int64_t)sms / threads, p.seqlen / 16);
+    const int64_t want = std::min<int64_t>(2 * cta.resident * (int64_t)sms / threads, p.seqlen / 16);
     if (want < 2) return pl;
     int64_t len = (p.seqlen + want - 1) / want;
     len = (len + 7) / 8 * 8;  // whole tiles
@@ -193,7 +193,7 @@ SSD_API ssd_status_t ssd_selective_scan(const ssd_scan_problem_t *prob, const ss
     p.vec_bc = states4(p.B, p.b_seq, p.b_tok) && states4(p.C, p.c_seq, p.c_tok);
     const size_t sa = (pr.dstate > 128 ? 8 : 4) * ses;
     p.vec_state = aligned(p.init, std::min<size_t>(sa, 16)) && aligned(p.fin, std::min<size_t>(sa, 16)) &&
-                  pr.dstate * ses % sa == 0;
+                  aligned(p.A, 16) && pr.dstate * ses % sa == 0;
     // a segment's CTA may read a sequence's initial state after another one wrote its final state: where the two
     // share memory the initial states are copied first
     if (pl.nseg > 1 && p.init && p.fin) {

@@ -88,15 +88,15 @@ template <int S, int TG> __device__ __forceinline__ void reduce_lanes(float (&v)
     }
 }
 
-// The last sequence whose start is at or before packed token t (empty ones before it share its start).
+// The last sequence whose start is at or before packed token t (empty ones before it share its start): the whole CTA
+// counts the starts, since a search would wait for memory at every step.
 __device__ __forceinline__ int64_t seq_at(const int32_t *cu, int64_t nseq, int64_t t) {
-    int64_t lo = 0, hi = nseq - 1;
-    while (lo < hi) {
-        const int64_t m = (lo + hi + 1) / 2;
-        if (cu[m] <= t) lo = m;
-        else hi = m - 1;
+    int64_t n = 0;
+    for (int64_t s = 0; s < nseq; s += blockDim.x) {
+        const int64_t i = s + threadIdx.x;
+        n += __syncthreads_count(i < nseq && cu[i] <= t);
     }
-    return lo;
+    return n > 0 ? n - 1 : 0;  // malformed offsets may start past t
 }
 
 template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_ = 512 / NT_> struct Shape {
@@ -250,13 +250,34 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
                                 c < clive && n + 1 < p.N ? f(c0 + ch + c, n + 1) : 0.f);
             }
     };
-    get2([&](int64_t c, int n) { return p.A[c * p.N + n] * kLog2e; });
+    // whole vectors of this lane's channels and states: rows of N at `base`
+    const bool vec_rows = p.vec_state && clive == kCH && n0 + R <= p.N;
+    auto get_rows = [&](const auto *base, int64_t i, int64_t n, uint32_t site) {  // i: the first channel's row
+        using E = typename std::remove_cv<typename std::remove_reference<decltype(*base)>::type>::type;
+#pragma unroll
+        for (int c = 0; c < kCH; ++c)
+#pragma unroll
+            for (int j = 0; j < R; j += 4) {
+                Raw<E, 4> r;
+                r.load(chk(base, (i + c) * p.N + n0 + j, 4, n, p.hdr, site));
+                const float2 u = r.pair(0), w = r.pair(2);
+                h[c][j / 2] = pack2(u.x, u.y);
+                h[c][j / 2 + 1] = pack2(w.x, w.y);
+            }
+    };
+    if (vec_rows) get_rows(p.A, c0 + ch, p.D_ * p.N, SITE_SCAN_STATE);
+    else get2([&](int64_t c, int n) { return p.A[c * p.N + n]; });
 #pragma unroll
     for (int c = 0; c < kCH; ++c)
 #pragma unroll
-        for (int i = 0; i < P; ++i) a[c][i] = h[c][i];
+        for (int i = 0; i < P; ++i) a[c][i] = mul2(h[c][i], pack2(kLog2e, kLog2e));
     auto initial = [&](int64_t s) {
-        get2([&](int64_t c, int n) { return p.init ? load_state(p, p.init, (s * p.D_ + c) * p.N + n) : 0.f; });
+        if (!p.init) get2([](int64_t, int) { return 0.f; });
+        else if (!vec_rows) get2([&](int64_t c, int n) { return load_state(p, p.init, (s * p.D_ + c) * p.N + n); });
+        else if (p.state_f16)
+            get_rows(static_cast<const __half *>(p.init), s * p.D_ + c0 + ch, p.nseq * p.D_ * p.N, SITE_SCAN_STATE);
+        else
+            get_rows(static_cast<const float *>(p.init), s * p.D_ + c0 + ch, p.nseq * p.D_ * p.N, SITE_SCAN_STATE);
     };
     auto each_state = [&](auto f) {  // f(c, n, h) for this lane's channels and states
 #pragma unroll
@@ -280,9 +301,11 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
         get2([](int64_t, int) { return 0.f; });
     } else {  // the state that enters this segment
         const int64_t i0 = (packed ? 0 : sq * (p.nseg - 1)) + k - 1;
-        get2([&](int64_t c, int n) {
-            return *chk(p.seg_state, (i0 * p.D_ + c) * p.N + n, 1, extent, p.hdr, SITE_SCAN_SEG);
-        });
+        if (vec_rows) get_rows(static_cast<const float *>(p.seg_state), i0 * p.D_ + c0 + ch, extent, SITE_SCAN_SEG);
+        else
+            get2([&](int64_t c, int n) {
+                return *chk(p.seg_state, (i0 * p.D_ + c) * p.N + n, 1, extent, p.hdr, SITE_SCAN_SEG);
+            });
     }
 
     // places of a two-channel unit in a row of du, of a four-channel unit in a row of ys: threads that write and threads
@@ -474,6 +497,8 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
 
 // seg_state[i], the leaving state of segment i from a zero state -> from its true entering state (which is what enters
 // segment i + 1). A thread takes one state of a channel through the segments of a sequence (packed: of the axis).
+constexpr int kJoin = 16;
+
 static __global__ void __launch_bounds__(256) join_kernel(ScanParams p) {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, dn = p.D_ * p.N;
     const int64_t chains = p.cu ? 1 : p.nseq, segs = p.nseg - 1;
@@ -483,12 +508,20 @@ static __global__ void __launch_bounds__(256) join_kernel(ScanParams p) {
     const int64_t extent = p.seg_items * dn;
     (void)extent;
     float h = *chk(p.seg_state, base * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
-#pragma unroll 4
-    for (int64_t j = 1; j < segs; ++j) {
-        float *s = chk(p.seg_state, (base + j) * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
-        const float d = p.seg_dt[(base + j) * p.D_ + c], v = *s;
-        h = d != d ? v : fmaf(ex2(a * d), h, v);
-        *s = h;
+    for (int64_t j0 = 1; j0 < segs; j0 += kJoin) {  // kJoin segments on their way at a time
+        float v[kJoin], d[kJoin];
+        float *s = chk(p.seg_state, (base + j0) * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
+        const float *sd = p.seg_dt + (base + j0) * p.D_ + c;
+        const int n = (int)(segs - j0 < kJoin ? segs - j0 : kJoin);
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+            if (j < n) v[j] = s[j * dn], d[j] = sd[j * p.D_];
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+            if (j < n) {
+                h = d[j] != d[j] ? v[j] : fmaf(ex2(a * d[j]), h, v[j]);
+                s[j * dn] = h;
+            }
     }
 }
 
@@ -685,7 +718,7 @@ using Shape256 = Shape<32, 8, 2, 256, 8, 2>;
 
 template <typename IO, typename T> cudaError_t launch_checked(const ScanParams &p, cudaStream_t stream) {
     const ScanCta c = scan_cta(p.N);
-    return c.channels == T::CT && c.threads == T::NT ? launch_shape<IO, T>(p, stream) : cudaErrorInvalidValue;
+    return c.channels == T::CT && c.threads == T::NT && c.resident == T::MINB * T::NT ? launch_shape<IO, T>(p, stream) : cudaErrorInvalidValue;
 }
 
 template <typename IO> cudaError_t launch_io(const ScanParams &p, cudaStream_t stream) {
