@@ -39,15 +39,54 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-// acc += s * r, 16 columns
-__device__ __forceinline__ void add16(float *acc, const uint32_t (&r)[16], float2 s) {
+// Warp-collective: 64 consecutive columns of the calling warp's TMEM lanes.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait64(uint32_t (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]),
+                   "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]),
+                   "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]), "+r"(r[49]),
+                   "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]), "+r"(r[56]),
+                   "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+                 :
+                 : "memory");
+}
+// acc += s * r, C columns
+template <int C> __device__ __forceinline__ void add_scaled(float *acc, const uint32_t (&r)[C], float2 s) {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < C; j += 2) {
         const float2 v = fma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s,
                               make_float2(acc[j], acc[j + 1]));
         acc[j] = v.x;
         acc[j + 1] = v.y;
     }
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1)
+                 : "memory");
 }
 
 // Bounded wait on a barrier's phase; on timeout it records SSD_ERR_DEVICE and raises the CTA's abort flag, after which
@@ -128,7 +167,7 @@ __device__ __forceinline__ Tile wide_tile(int64_t t, int64_t mt, int64_t nt) {
 template <typename OUT>
 __global__ void __launch_bounds__(kWThreads, 1)
     wide_kernel(MatmulParams p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                int vec) {
+                const __grid_constant__ CUtensorMap map_o, int vec) {
     extern __shared__ uint8_t dyn[];
     __shared__ WideBars sm;
     uint8_t *stages = dyn + (1024 - (smem_u32(dyn) & 1023)) % 1024;
@@ -191,27 +230,21 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 tc_fence_after();
                 const uint32_t at = tmem + ts * 256 + half * 128 + ((uint32_t)(q * 32) << 16);
                 const float2 s2 = make_float2(s, s);
-                uint32_t r0[16], r1[16];
-                tmem_ld16(at, r0);
-#pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    tmem_ld_wait16(r0);
-                    tmem_ld16(at + 16 * (c + 1), r1);
-                    add16(&acc[c * 16], r0, s2);
-                    tmem_ld_wait16(r1);
-                    if (c < 6) {
-                        tmem_ld16(at + 16 * (c + 2), r0);
-                    } else {  // this warp has read the block
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.tempty[ts]);
-                    }
-                    add16(&acc[c * 16 + 16], r1, s2);
-                }
+                uint32_t r[64];
+                tmem_ld64(at, r);
+                tmem_ld_wait64(r);
+                add_scaled(&acc[0], r, s2);
+                tmem_ld64(at + 64, r);
+                tmem_ld_wait64(r);
+                tc_fence_before();  // this warp has read the block
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.tempty[ts]);
+                add_scaled(&acc[64], r, s2);
             }
             if (!ok) break;
-            // out of registers through a 4 KB buffer of the warp (rows of 128 bytes, 16-byte pieces swizzled), so
-            // that rows are stored in 128-byte runs
+            // Out of registers through a 4 KB buffer of the warp (rows of 128 bytes, 16-byte pieces swizzled as a TMA
+            // store expects them); rows and columns past the end are clipped by the store. Rows that are no 16-byte
+            // multiples are stored piece by piece.
             constexpr int E = 16 / (int)sizeof(OUT), CW = 8 * E;  // elements of a piece, of a row of the buffer
 #pragma unroll
             for (int c = 0; c < 128 / CW; ++c) {
@@ -219,12 +252,25 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
                     for (int j = 0; j < CW; ++j)
                         if (n0 + c * CW + j < p.n) acc[c * CW + j] += p.bias[n0 + c * CW + j];
+                if (vec) {  // the store before this one has read the buffer
+                    if (lane == 0) bulk_wait_read0();
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                         pack16<OUT>(&acc[c * CW + j * E]);
+                if (vec) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && n0 + c * CW < p.n && tl.m0 + q * 32 < p.m) {
+                        tma_store_2d(&map_o, buf, (int)(n0 + c * CW), (int)(tl.m0 + q * 32));
+                        bulk_commit();
+                    }
+                    continue;
+                }
                 __syncwarp();
-#pragma unroll
+#pragma unroll 1
                 for (int u = 0; u < 8; ++u) {
                     const int r = u * 4 + lane / 8, j = lane % 8;
                     const int64_t row = tl.m0 + q * 32 + r, col = n0 + c * CW + j * E;
@@ -233,19 +279,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
                         const int64_t left = p.n - col;
                         OUT *o = chk(static_cast<OUT *>(p.out), row * p.out_row + col, left < E ? left : E,
                                      (p.m - 1) * p.out_row + p.n, hdr, SITE_FP8_OUT);
-                        if (vec && left >= E) {
-                            *reinterpret_cast<uint4 *>(o) = w;
-                        } else {
-                            const OUT *e = reinterpret_cast<const OUT *>(&w);
+                        const OUT *e = reinterpret_cast<const OUT *>(&w);
 #pragma unroll
-                            for (int x = 0; x < E; ++x)
-                                if (x < left) o[x] = e[x];
-                        }
+                        for (int x = 0; x < E; ++x)
+                            if (x < left) o[x] = e[x];
                     }
                 }
                 __syncwarp();
             }
         }
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0 && lane == 0) {
@@ -547,8 +591,24 @@ cudaError_t launch_wide(const MatmulParams &p, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k, smem, done);
     if (e != cudaSuccess) return e;
-    const int vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_row * sizeof(OUT))) & 15) == 0;
-    k<<<(unsigned)std::min<int64_t>(tiles, sms), kWThreads, smem, stream>>>(p, ma, mb, vec);
+    // output map [m, n], box [32, 128 bytes], where rows lie on 16-byte boundaries
+    int vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_row * sizeof(OUT))) & 15) == 0;
+    CUtensorMap mo = ma;
+    if (vec) {
+        const cuuint64_t dims[2] = {(cuuint64_t)p.n, (cuuint64_t)p.m};
+        const cuuint64_t strides[1] = {(cuuint64_t)(p.m > 1 ? p.out_row * sizeof(OUT) : (p.n * sizeof(OUT) + 15) / 16 * 16)};
+        const cuuint32_t box[2] = {128 / (cuuint32_t)sizeof(OUT), 32};
+        const cuuint32_t estr[2] = {1, 1};
+        const CUtensorMapDataType dt = sizeof(OUT) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : std::is_same<OUT, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        if (strides[0] >> 40 ||
+            encode_tiled_fn()(&mo, dt, 2, p.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            vec = 0;
+    }
+    k<<<(unsigned)std::min<int64_t>(tiles, sms), kWThreads, smem, stream>>>(p, ma, mb, mo, vec);
     return cudaGetLastError();
 }
 
