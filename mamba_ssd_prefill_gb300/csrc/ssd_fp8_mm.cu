@@ -7,9 +7,12 @@
 // tensor cores work on the next block in the other half of TMEM.
 //
 // Two kernels. wide_kernel: tokens are the 128 rows (TMEM lanes) of a tile, 256 weights its columns; one persistent
-// CTA per SM, TMA into four stages of 48 KB. narrow_kernel, for few tokens: weights are the 128 rows and TN tokens
-// the columns, so no row of the tensor core idles; K is split over the CTAs of a cluster, whose partial sums are
-// joined through distributed shared memory in rank order (no atomics: the result does not depend on timing).
+// CTA per SM, TMA into four stages of 48 KB, two blocks in TMEM. What bounds it is the turn of a TMEM half: MMA (512
+// clocks), read, FMA and back, so a warp reads 64 columns at a time and gives the half back before it adds them (16
+// columns at a time 16384 x 10576 x 2560 took 369 us, so 341: 2.6 PFLOP/s, under the power cap; 16384 x 8192 x 8192: 2.8).
+// narrow_kernel, for few tokens: weights are the 128 rows and TN tokens the columns, so no row of the tensor core idles;
+// K is split over the CTAs of a cluster, whose partial sums are joined through distributed shared memory in rank order
+// (no atomics: the result does not depend on timing). 16 x 10576 x 2560: 7.3 us, the weights at 3.7 TB/s.
 #include "sm100_ptx.cuh"
 #include "ssd_internal.h"
 #include "ssd_layer.cuh"
@@ -637,25 +640,31 @@ cudaError_t launch_narrow(const MatmulParams &p, int splits, cudaStream_t stream
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// The kernel and split whose estimated time is least, in clocks of one SM. A block of K costs the wide kernel 512
-// clocks a tile (its tensor-core time), the narrow one its bytes at about 64 a clock; two narrow CTAs share an SM.
+// The kernel and split whose estimated time is least, in nanoseconds. Measured on 16 sizes (1 .. 1024 tokens, K 640 ..
+// 8192, 640 .. 10576 outputs), each kernel and split forced in turn: a wave of the wide kernel takes 2.2 us and 0.375 a
+// block of K; a narrow CTA 1.6 us and 0.17, 0.24, 0.34 or 0.6 a block for 16 .. 128 tokens, half as much again where two
+// share an SM; the estimate then picks the fastest or one within 8 % of it (256 x 2560 x 5120: 64 tokens in 2 splits
+// 16.1 us, 128 in 4 15.4, wide 20.0; 128 x 10576 x 2560: wide 12.9, 64 tokens 15.3).
 struct Choice {
     int tn, splits;  // tn 0: wide
 };
 Choice choose(const MatmulParams &p, int sms) {
     const int64_t nkb = (p.k + kBK - 1) / kBK;
-    const double wide = (double)((((p.m + 127) / 128) * ((p.n + 255) / 256) + sms - 1) / sms) * (512.0 * nkb + 3000) + 2500;
+    const int64_t waves = (((p.m + 127) / 128) * ((p.n + 255) / 256) + sms - 1) / sms;
     Choice best{0, 1};
-    double least = wide;
-    for (int tn = 16; tn <= 128; tn *= 2) {
-        const int64_t tiles = ((p.m + tn - 1) / tn) * ((p.n + 127) / 128);
-        if ((p.m + tn - 1) / tn > 65535) continue;
+    double least = 2000.0 + (double)waves * (2200.0 + 375.0 * (double)nkb);
+    const double block_ns[4] = {170, 240, 340, 600}, shared[4] = {1.2, 1.5, 1.4, 1.75};
+    for (int i = 0, tn = 16; tn <= 128; ++i, tn *= 2) {
+        const int64_t mt = (p.m + tn - 1) / tn, tiles = mt * ((p.n + 127) / 128);
+        if (mt > 65535) continue;
         for (int splits = 1; splits <= 8; splits *= 2) {
             if (splits > 1 && splits * 2 > nkb) break;
             const int64_t blocks = (nkb + splits - 1) / splits;
             if (blocks * tn > kNScales || tiles * splits > (1 << 30)) continue;
             const int64_t on_sm = (tiles * splits + sms - 1) / sms;  // CTAs an SM gets, two at a time
-            const double t = (double)blocks * (256 + 2 * tn) * on_sm + ((on_sm + 1) / 2) * 3000 + 500 + 200 * splits;
+            const double t = 3000.0 + (splits > 1 ? 500.0 + 100.0 * splits : 0.0) +
+                             (double)((on_sm + 1) / 2) *
+                                 (1600.0 + block_ns[i] * (double)blocks * (on_sm > 1 ? shared[i] : 1.0));
             if (t < least) {
                 least = t;
                 best = Choice{tn, splits};
