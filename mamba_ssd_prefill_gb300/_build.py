@@ -1,4 +1,4 @@
-"""Build step of the CUDA library: nvcc for sm_103a, one shared object, in-tree."""
+"""Build step of the CUDA library (nvcc for sm_103a, one shared object, in-tree) and of the Python binding in C++."""
 from __future__ import annotations
 
 import os
@@ -10,6 +10,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmamba_ssd.so")
+BINDING = os.path.join(PKG, "_layer.so")  # Python binding of the operators around the SSD (csrc/layer_binding.cpp)
 LIB_CHECKED = os.path.join(PKG, "libmamba_ssd_checked.so")  # debug build: every kernel's global indices range-checked
 SOURCES = ["ssd_api.cu", "ssd_simt.cu", "ssd_tc.cu", "ssd_step.cu", "ssd_varlen.cu", "ssd_conv.cu", "ssd_noalloc.cu", "ssd_host.cu",
            "ssd_segstate.cu", "ssd_layer_api.cu", "ssd_selscan_f32.cu", "ssd_selscan_bf16.cu", "ssd_selscan_f16.cu", "ssd_rowconv.cu", "ssd_norm.cu", "ssd_fp8.cu", "ssd_fp8_mm.cu"]
@@ -24,6 +25,28 @@ def nvcc() -> str:
 def flags(extra=()):
     return [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
             "-I", os.path.join(ROOT, "include"), *extra]
+
+
+def build_binding() -> str:
+    """Compile the binding against this Python and PyTorch (host code; it calls the library that the package loads)."""
+    import sysconfig
+
+    import torch
+
+    torch_dir = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+           "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "layer_binding.cpp"), "-o", tmp, "-L", os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(torch_dir, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding failed to compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, checked: bool = False) -> str:
@@ -46,8 +69,11 @@ def build(verbose: bool = False, ptxas_info: bool = False, checked: bool = False
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = None if checked else ex.submit(build_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        if binding:
+            binding.result()
     tmp = out + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
