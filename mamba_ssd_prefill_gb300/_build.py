@@ -13,7 +13,7 @@ LIB = os.path.join(PKG, "libmamba_ssd.so")
 BINDING = os.path.join(PKG, "_layer.so")  # Python binding of the operators around the SSD (csrc/layer_binding.cpp)
 LIB_CHECKED = os.path.join(PKG, "libmamba_ssd_checked.so")  # debug build: every kernel's global indices range-checked
 SOURCES = ["ssd_api.cu", "ssd_simt.cu", "ssd_tc.cu", "ssd_step.cu", "ssd_varlen.cu", "ssd_conv.cu", "ssd_noalloc.cu", "ssd_host.cu",
-           "ssd_segstate.cu", "ssd_layer_api.cu", "ssd_selscan_f32.cu", "ssd_selscan_bf16.cu", "ssd_selscan_f16.cu", "ssd_rowconv.cu", "ssd_norm.cu", "ssd_fp8.cu", "ssd_fp8_mm.cu"]
+           "ssd_segstate.cu", "ssd_layer_api.cu", "ssd_selscan_f32.cu", "ssd_selscan_bf16.cu", "ssd_selscan_f16.cu", "ssd_rowconv.cu", "ssd_norm_f32.cu", "ssd_norm_bf16.cu", "ssd_norm_f16.cu", "ssd_fp8.cu", "ssd_fp8_mm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

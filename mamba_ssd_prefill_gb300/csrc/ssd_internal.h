@@ -153,7 +153,10 @@ struct NormParams {
     int vec;  // 16-byte pieces of every group of x, z, y, w and bias are aligned
     float eps;
 };
-cudaError_t launch_norm(const NormParams &p, int io_dtype, int sms, cudaStream_t stream);
+// ssd_norm.cuh, one translation unit per type
+cudaError_t launch_norm_f32(const NormParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_norm_bf16(const NormParams &p, int sms, cudaStream_t stream);
+cudaError_t launch_norm_f16(const NormParams &p, int sms, cudaStream_t stream);
 
 struct QuantParams {
     const void *x;

@@ -317,8 +317,11 @@ SSD_API ssd_status_t ssd_group_norm(const ssd_norm_problem_t *prob, const ssd_no
     const int64_t vec = 16 / (int64_t)es, gs = pr.channels / pr.ngroups;  // 16-byte pieces of every group
     p.vec = gs % vec == 0 && aligned(p.x, 16) && aligned(p.z, 16) && aligned(p.y, 16) && aligned(p.w, 16) &&
             aligned(p.bias, 16) && (pr.rows == 1 || (p.x_row % vec == 0 && p.z_row % vec == 0 && p.y_row % vec == 0));
-    return ssd::launch_norm(p, pr.io_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK
-                                                                                                  : SSD_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = pr.io_dtype == SSD_F32    ? ssd::launch_norm_f32(p, sms, s)
+                          : pr.io_dtype == SSD_BF16 ? ssd::launch_norm_bf16(p, sms, s)
+                                                    : ssd::launch_norm_f16(p, sms, s);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 SSD_API ssd_status_t ssd_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, int32_t io_dtype, const void *x,
