@@ -172,21 +172,19 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) norm_kernel(NormParams p, 
     for (; row < p.rows; parity ^= 1) {
         const int64_t c0 = grp * gs;
         float2 v[P];
-        Raw<IO, V> gate[GATE == kAfter ? NV : 1];
+        Raw<IO, V> gate[GATE != kNone ? NV : 1];
         auto act2 = [&](float2 u) { return p.silu ? silu2(u) : u; };
-        if constexpr (GATE == kFirst) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) v[k] = mul2(value(rx, k), act2(value(rz, k)));
-        } else {
+        for (int k = 0; k < P; ++k) v[k] = value(rx, k);
+        if constexpr (GATE != kNone)
 #pragma unroll
-            for (int k = 0; k < P; ++k) v[k] = value(rx, k);
-            if constexpr (GATE == kAfter)
-#pragma unroll
-                for (int i = 0; i < NV; ++i) gate[i] = rz[i];
-        }
+            for (int i = 0; i < NV; ++i) gate[i] = rz[i];
         int64_t next_row = row + step_row, next_grp = grp + step_grp;
         if (next_grp >= p.G) next_grp -= p.G, ++next_row;
-        load(next_row, next_grp);  // under this token's sums
+        load(next_row, next_grp);  // under this token's arithmetic
+        if constexpr (GATE == kFirst)
+#pragma unroll
+            for (int k = 0; k < P; ++k) v[k] = mul2(v[k], act2(value(gate, k)));
         if (p.center) {
             float2 s = make_float2(0.f, 0.f);
 #pragma unroll
