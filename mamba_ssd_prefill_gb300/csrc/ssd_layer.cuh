@@ -77,6 +77,11 @@ template <typename IO, int K> struct Raw {
             }
         }
     }
+    __device__ __forceinline__ void store(IO *p) const {  // all K, 16 bytes at a time
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
     // the first n of K elements (the others zero); vec: p is aligned for K elements
     __device__ __forceinline__ void load(const IO *p, int n, bool vec) {
         if (vec && n >= K) {

@@ -176,15 +176,17 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) norm_kernel(NormParams p, 
         auto act2 = [&](float2 u) { return p.silu ? silu2(u) : u; };
 #pragma unroll
         for (int k = 0; k < P; ++k) v[k] = value(rx, k);
-        if constexpr (GATE != kNone)
+        if constexpr (GATE != kNone) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) gate[i] = rz[i];
+        }
         int64_t next_row = row + step_row, next_grp = grp + step_grp;
         if (next_grp >= p.G) next_grp -= p.G, ++next_row;
         load(next_row, next_grp);  // under this token's arithmetic
-        if constexpr (GATE == kFirst)
+        if constexpr (GATE == kFirst) {
 #pragma unroll
             for (int k = 0; k < P; ++k) v[k] = mul2(v[k], act2(value(gate, k)));
+        }
         if (p.center) {
             float2 s = make_float2(0.f, 0.f);
 #pragma unroll

@@ -9,7 +9,8 @@
 // and quarter for the recurrence alone. So the states stay in registers, and what is around it is kept small:
 //
 //  - A CTA owns CT channels (of one group) and walks tokens in tiles of TT. A tile's x, dt and z are copied to shared
-//    memory one tile ahead (16-byte asynchronous copies); each thread turns the vectors that it copied into (dt, dt x)
+//    memory one tile ahead (16-byte asynchronous copies, or through registers where rows are not 16-byte multiples); each
+//    thread turns the vectors that it copied into (dt, dt x)
 //    per token and channel, B and C are kept in fp32. The softplus is so taken once per (token, channel).
 //  - A thread holds CH channels x R states in packed pairs, S lanes share the states of its channels. A shared memory
 //    load costs its bytes per lane, broadcast or not (an LDS.128 four cycles of the SM's pipe), and B and C are eight
@@ -110,8 +111,8 @@ template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_ = 512 / NT_> stru
     }
 };
 
-template <typename IO, typename T, bool SUM>
-__global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
+template <typename IO, typename T, bool SUM, bool VEC>
+__global__ void __launch_bounds__(T::NT, VEC || T::MINB < 2 ? T::MINB : T::MINB - 1) scan_kernel(ScanParams p) {
     constexpr int S = T::S, R = T::R, NT = T::NT, TT = T::TT, CT = T::CT, NP = T::NP, CV = T::CV, VPT = T::VPT,
                   NV = T::NV, P = R / 2, kCH = T::CH;
     constexpr int BPT = (TT * NV * (SUM ? 1 : 2) + NT - 1) / NT;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
         return (const IO *)chk(w, base + off - w, n, extent, p.hdr, SITE_SCAN_IN);
     };
     auto copy = [&](IO *dst, const IO *src) {
-        if (p.vec && vlive == 8) {
+        if (vlive == 8) {
 #pragma unroll
             for (int i = 0; i < (int)sizeof(IO) / 2; ++i)
                 cp_async16(reinterpret_cast<uint8_t *>(dst) + 16 * i, reinterpret_cast<const uint8_t *>(src) + 16 * i);
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
     // element offsets of this thread's first vectors in the tile that is copied next, stepped from tile to tile
     int64_t ox = (t0 + trow) * p.x_tok + cv, od = (t0 + trow) * p.dt_tok + cv, oz = (t0 + trow) * p.z_tok + cv;
     const int b_t = tid / NV % TT, b_n = tid % NV * 4;
+    Raw<IO, 8> ahead[VEC ? 1 : SUM ? 2 : 3][VEC ? 1 : VPT];
     auto load = [&](int64_t tile, int stage) {
         IO *st = raw + stage * (SUM ? 2 : 3) * RAW + trow * CT + cv;
         const int n = (int)(t1 - tile < TT ? t1 - tile : TT);
@@ -211,9 +213,18 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
         for (int v = 0; v < VPT; ++v) {
             const int t = trow + v * TSTEP;
             if (t < n && vlive > 0) {
-                copy(st + v * TSTEP * CT, at(x, p.x, ox + v * TSTEP * p.x_tok, vlive, xn));
-                copy(st + RAW + v * TSTEP * CT, at(dt, p.dt, od + v * TSTEP * p.dt_tok, vlive, dn));
-                if (!SUM && z) copy(st + 2 * RAW + v * TSTEP * CT, at(z, p.z, oz + v * TSTEP * p.z_tok, vlive, zn));
+                const IO *px = at(x, p.x, ox + v * TSTEP * p.x_tok, vlive, xn);
+                const IO *pd = at(dt, p.dt, od + v * TSTEP * p.dt_tok, vlive, dn);
+                const IO *pz = !SUM && z ? at(z, p.z, oz + v * TSTEP * p.z_tok, vlive, zn) : nullptr;
+                if constexpr (VEC) {
+                    copy(st + v * TSTEP * CT, px);
+                    copy(st + RAW + v * TSTEP * CT, pd);
+                    if (!SUM && pz) copy(st + 2 * RAW + v * TSTEP * CT, pz);
+                } else {  // element by element, to registers: on their way while the tile before is worked on
+                    ahead[0][v].load(px, vlive, false);
+                    ahead[1][v].load(pd, vlive, false);
+                    if (!SUM && pz) ahead[SUM ? 1 : 2][v].load(pz, vlive, false);
+                }
             }
         }
         ox += TT * p.x_tok;
@@ -378,7 +389,18 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
         const int n = (int)(t1 - tile < TT ? t1 - tile : TT);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (tile == t0) __syncthreads();  // bias_s and D_s
-        const IO *st = raw + stage * (SUM ? 2 : 3) * RAW;
+        IO *st = raw + stage * (SUM ? 2 : 3) * RAW;
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int t = trow + v * TSTEP;
+                if (t < n && vlive > 0) {
+                    ahead[0][v].store(st + t * CT + cv);
+                    ahead[1][v].store(st + RAW + t * CT + cv);
+                    if (!SUM && z) ahead[SUM ? 1 : 2][v].store(st + 2 * RAW + t * CT + cv);
+                }
+            }
+        }
         // (dt, dt x); tokens past the end: a decay of 1 and nothing added
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
@@ -463,7 +485,7 @@ __global__ void __launch_bounds__(T::NT, T::MINB) scan_kernel(ScanParams p) {
                             o[i + 1] *= silu_f32(g.y);
                         }
                     IO *out = chk(static_cast<IO *>(p.y), oy + v * TSTEP * p.y_tok, vlive, yn, p.hdr, SITE_SCAN_Y);
-                    if (p.vec && vlive == 8) {
+                    if (VEC && vlive == 8) {
                         Raw<IO, 8> w;
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) w.set_pair(i, o[i], o[i + 1]);
@@ -667,11 +689,11 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
         body(std::integral_constant<bool, false>());
 }
 
-template <typename IO, typename T, bool SUM>
+template <typename IO, typename T, bool SUM, bool VEC>
 cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream) {
     const int64_t grid = items * ((p.cpg + T::CT - 1) / T::CT) * p.G;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    auto k = scan_kernel<IO, T, SUM>;
+    auto k = scan_kernel<IO, T, SUM, VEC>;
     constexpr size_t smem = T::smem(SUM, sizeof(IO));
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> done{0};
@@ -684,7 +706,8 @@ cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream)
 template <typename IO, typename T>
 cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
     if (p.nseg > 1) {
-        cudaError_t e = launch_pass<IO, T, true>(p, p.seg_items, stream);
+        cudaError_t e = p.vec ? launch_pass<IO, T, true, true>(p, p.seg_items, stream)
+                              : launch_pass<IO, T, true, false>(p, p.seg_items, stream);
         if (e != cudaSuccess) return e;
         if (p.nseg > 2) {
             const int64_t grid = ((p.cu ? 1 : p.nseq) * p.D_ * p.N + 255) / 256;
@@ -694,7 +717,8 @@ cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
             if (e != cudaSuccess) return e;
         }
     }
-    return launch_pass<IO, T, false>(p, p.cu ? p.nseg : p.nseq * p.nseg, stream);
+    const int64_t items = p.cu ? p.nseg : p.nseq * p.nseg;
+    return p.vec ? launch_pass<IO, T, false, true>(p, items, stream) : launch_pass<IO, T, false, false>(p, items, stream);
 }
 template <typename IO, int S, int R>
 cudaError_t launch_step_kernel(const ScanParams &p, cudaStream_t stream) {
