@@ -77,6 +77,18 @@ template <typename IO, int K> struct Raw {
             }
         }
     }
+    // all K elements, one by one
+    __device__ __forceinline__ void load_each(const IO *p) {
+        IO e[K];
+#pragma unroll
+        for (int i = 0; i < K; ++i) e[i] = p[i];
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            if constexpr (sizeof(IO) == 4) w[i] = bits(e[i]);
+            else if (i % 2 == 0) w[i / 2] = bits(e[i]);
+            else w[i / 2] |= bits(e[i]) << 16;
+        }
+    }
     __device__ __forceinline__ void store(IO *p) const {  // all K, 16 bytes at a time
 #pragma unroll
         for (int i = 0; i < W / 4; ++i)
