@@ -10,6 +10,7 @@ namespace {
 // One warp per block of block_rows x 128 elements.
 template <typename IO>
 __global__ void __launch_bounds__(256) quantize_kernel(QuantParams p) {
+    after_previous();
     const int lane = threadIdx.x % 32;
     const int64_t kb = (p.cols + 127) / 128, rb = (p.rows + p.block_rows - 1) / p.block_rows;
     const IO *x = static_cast<const IO *>(p.x);
@@ -41,6 +42,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantParams p) {
     const IO *x = static_cast<const IO *>(p.x);
     const int64_t xn = (p.rows - 1) * p.x_row + p.cols;
     (void)xn;
+    after_previous();
     Raw<IO, 8> r[N];
     int64_t col0, row0 = quick_div(b0, kb, col0), row = row0, col = col0;
 #pragma unroll
@@ -81,17 +83,14 @@ template <typename IO> cudaError_t launch_t(const QuantParams &p, int sms, cudaS
     const int64_t blocks = (p.rows + p.block_rows - 1) / p.block_rows * ((p.cols + 127) / 128);
     if (p.block_rows == 1 && p.vec) {
         if (blocks < (int64_t)sms * 64) {  // few blocks: one a half-warp
-            quantize_rows_kernel<IO, 1><<<(unsigned)((blocks + 15) / 16), 256, 0, stream>>>(p);
-            return cudaGetLastError();
+            return launch_after(quantize_rows_kernel<IO, 1>, (blocks + 15) / 16, 256, 0, stream, p);
         }
         const int64_t grid = (blocks + 63) / 64;
         if (grid > INT32_MAX) return cudaErrorInvalidValue;
-        quantize_rows_kernel<IO, 4><<<(unsigned)grid, 256, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_after(quantize_rows_kernel<IO, 4>, grid, 256, 0, stream, p);
     }
     const int64_t grid = std::min<int64_t>((blocks + 7) / 8, (int64_t)sms * 64);
-    quantize_kernel<IO><<<(unsigned)grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(quantize_kernel<IO>, grid, 256, 0, stream, p);
 }
 
 }  // namespace

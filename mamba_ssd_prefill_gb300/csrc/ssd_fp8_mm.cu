@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
+    after_previous();
 
     if (warp >= 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kNThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
+    after_previous();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -567,6 +569,7 @@ __global__ void __launch_bounds__(kNThreads)
 // k = 0: the bias, or zeros
 template <typename OUT>
 __global__ void __launch_bounds__(256) bias_kernel(MatmulParams p) {
+    after_previous();
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < p.m * p.n; e += (int64_t)gridDim.x * 256)
         static_cast<OUT *>(p.out)[e / p.n * p.out_row + e % p.n] = from_f32<OUT>(p.bias ? p.bias[e % p.n] : 0.f);
 }
@@ -611,7 +614,11 @@ cudaError_t launch_wide(const MatmulParams &p, int sms, cudaStream_t stream) {
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             vec = 0;
     }
-    k<<<(unsigned)std::min<int64_t>(tiles, sms), kWThreads, smem, stream>>>(p, ma, mb, mo, vec);
+    // Many waves start once the kernel before has ended: started as its CTAs leave, the CTAs of neighbouring tiles land on
+    // SMs apart (quantiser and product, 16384 x 2560 x 10576: 410 us against 401; 8191 x 5120 x 2560 behind the norm,
+    // four waves: 157 against 160).
+    if (tiles < (int64_t)sms * 8) return launch_after(k, std::min<int64_t>(tiles, sms), kWThreads, smem, stream, p, ma, mb, mo, vec);
+    k<<<(unsigned)sms, kWThreads, smem, stream>>>(p, ma, mb, mo, vec);
     return cudaGetLastError();
 }
 
@@ -628,12 +635,14 @@ cudaError_t launch_narrow(const MatmulParams &p, int splits, cudaStream_t stream
     cfg.blockDim = dim3(kNThreads);
     cfg.dynamicSmemBytes = Narrow<TN>::kDyn;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)splits;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const size_t align = 4 * sizeof(OUT);
     const int vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_row * sizeof(OUT))) & (align - 1)) == 0;
     e = cudaLaunchKernelEx(&cfg, k, p, mw, mt, splits, vec);
@@ -677,8 +686,8 @@ Choice choose(const MatmulParams &p, int sms) {
 template <typename OUT>
 cudaError_t launch_t(const MatmulParams &p, int sms, cudaStream_t stream) {
     if (p.k == 0) {
-        bias_kernel<OUT><<<(unsigned)std::min<int64_t>((p.m * p.n + 255) / 256, (int64_t)sms * 8), 256, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_after(bias_kernel<OUT>, std::min<int64_t>((p.m * p.n + 255) / 256, (int64_t)sms * 8), 256, 0, stream,
+                            p);
     }
     const Choice c = choose(p, sms);
     switch (c.tn) {

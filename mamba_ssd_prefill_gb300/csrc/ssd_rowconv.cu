@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
     constexpr int KH = K > 1 ? K - 1 : 1, P = V > 1 ? V / 2 : 1, G = V > 1 ? 4 : 8;  // P: channel pairs, G: tokens a stage
     __shared__ uint4 ring[V > 1 ? kStages * G : 1][V > 1 ? kThreads : 1];
     const int64_t nvec = p.D / V, idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    after_previous();
     if (p.cu && blockIdx.x == 0) check_offsets(p.cu, p.nseq, p.T, p.hdr);
     int64_t cvec;
     const int64_t item = quick_div(idx, nvec, cvec), c = cvec * V;
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
 // (sequence, channel): its old entries are read before any is written.
 template <typename IO>
 __global__ void __launch_bounds__(kThreads) row_conv_state_kernel(RowConvParams p) {
+    after_previous();
     const int64_t total = p.nseq * p.D;
     const IO *x = static_cast<const IO *>(p.x);
     const IO *state = static_cast<const IO *>(p.state);
@@ -331,8 +333,7 @@ template <typename IO, int K, int V>
 cudaError_t launch_kv(const RowConvParams &p, int tl, int64_t tiles, int write_state, cudaStream_t stream) {
     const int64_t threads = (p.cu ? tiles : p.nseq * tiles) * (p.D / V), grid = (threads + kThreads - 1) / kThreads;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    row_conv_kernel<IO, K, V><<<(unsigned)grid, kThreads, 0, stream>>>(p, tl, tiles, write_state);
-    return cudaGetLastError();
+    return launch_after(row_conv_kernel<IO, K, V>, grid, kThreads, 0, stream, p, tl, tiles, write_state);
 }
 template <typename IO, int V>
 cudaError_t launch_v(const RowConvParams &p, int tl, int64_t tiles, int write_state, cudaStream_t stream) {
@@ -369,8 +370,7 @@ cudaError_t launch_t(const RowConvParams &p, int sms, cudaStream_t stream) {
     }
     if (save_after) {
         const int64_t grid = std::min<int64_t>((p.nseq * p.D + kThreads - 1) / kThreads, (int64_t)sms * 64);
-        row_conv_state_kernel<IO><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_after(row_conv_state_kernel<IO>, grid, kThreads, 0, stream, p);
     }
     return cudaSuccess;
 }

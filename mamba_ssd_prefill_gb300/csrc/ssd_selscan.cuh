@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
     const int ch = tid / S * kCH, q = tid % S;                             // this thread's first channel, its lane's place
     const int clive = left - ch < 0 ? 0 : left - ch < kCH ? left - ch : kCH;
     const bool packed = p.cu != nullptr;
+    after_previous();
 
     // tokens [t0, t1) of sequence `sq` (packed: of the packed axis, sq the sequence that holds t0)
     int64_t sq, k, t0, t1, qe = 0;
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
 constexpr int kJoin = 16;
 
 static __global__ void __launch_bounds__(256) join_kernel(ScanParams p) {
+    after_previous();
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, dn = p.D_ * p.N;
     const int64_t chains = p.cu ? 1 : p.nseq, segs = p.nseg - 1;
     if (e >= chains * dn) return;
@@ -578,6 +580,7 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
     const int64_t total = p.nseq * p.D_ * p.N, seq_states = p.D_ * p.N;
     (void)total;
     const bool whole = nl >= R;
+    after_previous();
     const int mine = q * kSeqs / S;  // this lane discretises and gates for the sequences mine, mine + 1, ..
     const int64_t i0 = s0 * seq_states + cN + n0;
     const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, Dc = p.D ? p.D[cc] : 0.f;
@@ -711,8 +714,7 @@ cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream)
         const cudaError_t e = allow_smem(k, smem, done);
         if (e != cudaSuccess) return e;
     }
-    k<<<(unsigned)grid, T::NT, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(k, grid, T::NT, smem, stream, p);
 }
 template <typename IO, typename T>
 cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
@@ -723,8 +725,7 @@ cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
         if (p.nseg > 2) {
             const int64_t grid = ((p.cu ? 1 : p.nseq) * p.D_ * p.N + 255) / 256;
             if (grid > INT32_MAX) return cudaErrorInvalidValue;
-            join_kernel<<<(unsigned)grid, 256, 0, stream>>>(p);
-            e = cudaGetLastError();
+            e = launch_after(join_kernel, grid, 256, 0, stream, p);
             if (e != cudaSuccess) return e;
         }
     }
@@ -736,9 +737,8 @@ cudaError_t launch_step_kernel(const ScanParams &p, cudaStream_t stream) {
     constexpr int CT = 128 / S;
     const int64_t grid = (p.D_ + CT - 1) / CT * ((p.nseq + kSeqs - 1) / kSeqs);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    if (p.state_f16) step_kernel<IO, __half, S, R><<<(unsigned)grid, 128, 0, stream>>>(p);
-    else step_kernel<IO, float, S, R><<<(unsigned)grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.state_f16 ? launch_after(step_kernel<IO, __half, S, R>, grid, 128, 0, stream, p)
+                       : launch_after(step_kernel<IO, float, S, R>, grid, 128, 0, stream, p);
 }
 
 // By the number of states; scan_cta (ssd_internal.h) tells the planner their channels and threads.

@@ -622,6 +622,45 @@ def test_calls_on_another_stream():
 
 
 @gpu
+@pytest.mark.parametrize("L,Dc", [(1, 256), (3, 2560), (700, 512), (5000, 1536)])
+def test_calls_in_a_row_without_waiting(L, Dc):
+    """A kernel may start while the one before it still runs: chains through the same buffers, with work of other
+    kinds in between, give the same bits as with a wait after every call."""
+    t = scan_inputs(2, L, Dc, 16, seed=47)
+    w = torch.randn(Dc, 4, generator=gen(3)).cuda()
+    wq, ws = m.ssd_fp8_quantize(torch.randn(Dc, Dc, generator=gen(4)).cuda() / Dc ** 0.5, 128)
+
+    def chain(wait):
+        x, st, cache = t["x"].clone(), t["init_states"].clone(), torch.zeros(2, Dc, 3, dtype=BF16, device="cuda")
+        u, y = torch.empty_like(x), torch.empty_like(x)
+        done = torch.cuda.synchronize if wait else (lambda: None)
+        for i in range(6):
+            m.ssd_conv(x, w, None, cache, out=u, conv_state_out=cache)
+            done()
+            m.ssd_selective_scan(u, t["dt_raw"], t["dt_bias"], t["A"], t["B"], t["C"], t["D"], t["z"],
+                                 init_states=st, final_states=st, y=y)
+            done()
+            m.ssd_group_norm(y, z=u, y=y)
+            done()
+            if i % 2:
+                x.zero_()
+                done()
+            q, sc = m.ssd_fp8_quantize(y)
+            done()
+            m.ssd_fp8_matmul(q, sc, wq, ws, out=x)
+            done()
+            if i % 3 == 2:
+                x += u
+                done()
+        return x, st, cache
+
+    want = chain(True)
+    for _ in range(3):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+
+
+@gpu
 def test_decode_step_in_a_cuda_graph():
     """conv, scan, norm to e4m3 and projection of one token, captured and replayed on new inputs."""
     Dc, N = 256, 16
