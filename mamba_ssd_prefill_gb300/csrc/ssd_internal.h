@@ -101,25 +101,26 @@ struct ScanParams {
     int64_t nseq, L, T, D_, N, G, cpg;  // L: tokens of a sequence (packed: T); cpg: channels per group
     int64_t x_seq, x_tok, dt_seq, dt_tok, z_seq, z_tok, b_seq, b_tok, c_seq, c_tok, y_seq, y_tok;
     int softplus, state_f16;
-    int vec, vec_bc, vec_state;  // 8-channel vectors of x, dt, z, y, 4-state vectors of B, C, and states are aligned
+    int unit;                // bytes that x, dt, z and y are copied by: 16, 8, 4, or 0 (single elements)
+    int vec_bc, vec_state;   // 4-state vectors of B and C, and of states are aligned
     int64_t rows;                // leading dimension of the token tensors (packed: 1)
     // segments of seg_len tokens: nseg per sequence, packed: of the packed axis; the leaving states [seg_items, D, N] and
     // summed dt [seg_items, D] of all but each last one
     int64_t nseg, seg_len, seg_items;
     float *seg_state, *seg_dt;
 };
-// Channels and threads of a scan CTA, and the threads that an SM holds, by the number of states (the shapes in
-// ssd_selscan.cuh).
+// Channels and threads of a scan CTA, and the CTAs that an SM holds (of them where rows are copied by single elements),
+// by the number of states (the shapes in ssd_selscan.cuh).
 struct ScanCta {
-    int channels, threads, resident;
+    int channels, threads, resident, resident_single;
 };
 inline ScanCta scan_cta(int64_t N) {
-    if (N <= 4) return {128, 32, 512};
-    if (N <= 8) return {128, 64, 640};
-    if (N <= 16) return {128, 128, 640};
-    if (N <= 24) return {128, 128, 512};
-    if (N <= 32) return {128, 256, 512};
-    return {N <= 64 ? 64 : N <= 128 ? 32 : 16, 256, 512};
+    if (N <= 4) return {128, 32, 16, 12};
+    if (N <= 8) return {128, 64, 8, 7};
+    if (N <= 16) return {128, 128, 5, 4};
+    if (N <= 24) return {128, 128, 4, 3};
+    if (N <= 32) return {128, 256, 2, 1};
+    return {N <= 64 ? 64 : N <= 128 ? 32 : 16, 256, 2, 1};
 }
 // ssd_selscan.cuh, one translation unit per type
 cudaError_t launch_scan_f32(const ScanParams &p, cudaStream_t stream);

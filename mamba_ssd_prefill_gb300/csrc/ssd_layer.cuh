@@ -30,10 +30,10 @@ __device__ __forceinline__ void after_previous() {
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+cudaError_t launch_after(void (*kernel)(P...), int64_t grid, dim3 threads, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -170,6 +170,12 @@ template <typename IO, int K> struct Raw {
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
+template <int BYTES> __device__ __forceinline__ void cp_async(void *dst, const void *src) {  // 4 or 8
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES)
                  : "memory");
 }
 

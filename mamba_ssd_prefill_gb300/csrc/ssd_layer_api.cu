@@ -51,20 +51,25 @@ struct ScanPlan {
     int64_t nseg = 1, seg_len = 0, items = 0;  // items: segments whose leaving state is kept
     size_t state_off = 0, dt_off = 0, copy_off = 0, bytes = sizeof(WsHeader);
 };
-ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments) {
+// single: rows are copied by single elements (fewer CTAs are resident, and a plan never takes more workspace than without)
+ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments, bool single) {
     ScanPlan pl;
     const int64_t chains = p.packed ? 1 : p.batch;
     pl.seg_len = std::max<int64_t>(p.seqlen, 1);
     if (!segments || p.batch == 0 || (!p.packed && p.seqlen <= 1)) return pl;
     // Without segments the work of a chain runs once, with them its states' part twice. So segments are cut only where
     // the CTAs leave the SMs short of warps (under about 1.3 CTAs of 128 threads each: 4 x 4096 x 1536 x 16, 48 CTAs,
-    // 0.84 ms in one chain and 0.24 segmented; 32 x 4096 x 1536 x 16, 384 CTAs, 1.28 and 1.57 ms), and then so many that
-    // two waves of resident CTAs fill: fewer leave a ragged wave, more pay the entry of a segment.
+    // 0.84 ms in one chain and 0.24 segmented; 32 x 4096 x 1536 x 16, 384 CTAs, 1.28 and 1.57 ms when both were
+    // measured), and then so many that
+    // the resident CTAs are full once, or twice where segments are long: a part of a wave leaves SMs idle (8192 x 5120 x
+    // 16: 0.5, 1, 1.5 and 2 waves 0.70, 0.378, 0.416 and 0.379 ms; 16384 x 5120 x 16: 1 and 2 waves 0.736 and 0.728), and
+    // more segments pay their entry more often (4000 x 1536 x 16, packed: 1 and 2 waves 75 and 85 us).
     const ssd::ScanCta cta = ssd::scan_cta(p.dstate);
     const int64_t per_group = (p.channels / p.ngroups + cta.channels - 1) / cta.channels;
     const int64_t ctas = chains * p.ngroups * per_group, threads = ctas * cta.threads;
     if (threads * 10 >= 13 * 128 * (int64_t)sms) return pl;
-    const int64_t want = std::min<int64_t>(2 * cta.resident * (int64_t)sms / threads, p.seqlen / 16);
+    const int64_t wave = (int64_t)(single ? cta.resident_single : cta.resident) * sms / ctas;
+    const int64_t want = std::min<int64_t>(p.seqlen >= 2 * wave * 400 ? 2 * wave : wave, p.seqlen / 16);
     if (want < 2) return pl;
     int64_t len = (p.seqlen + want - 1) / want;
     len = (len + 7) / 8 * 8;  // whole tiles
@@ -88,7 +93,7 @@ SSD_API ssd_status_t ssd_selective_scan_workspace_size(const ssd_scan_problem_t 
     if (!bytes) return SSD_ERR_INVALID_ARG;
     const ssd_status_t st = check_scan(prob);
     if (st != SSD_OK) return st;
-    *bytes = plan_scan(*prob, std::max(1, ssd::device_sms()), true).bytes;
+    *bytes = plan_scan(*prob, std::max(1, ssd::device_sms()), true, false).bytes;
     return SSD_OK;
 }
 
@@ -171,20 +176,24 @@ SSD_API ssd_status_t ssd_selective_scan(const ssd_scan_problem_t *prob, const ss
     p.softplus = pr.softplus;
     p.state_f16 = pr.state_dtype == SSD_F16;
     p.rows = rows_seq;
-    ScanPlan pl = plan_scan(pr, sms, true);
-    if (workspace_bytes < pl.bytes) pl = plan_scan(pr, sms, false);  // too small for segments: one chain a sequence
+    const int64_t cpg_bytes = p.cpg * (int64_t)es;
+    auto rows_of = [&](const void *q, int64_t seq, int64_t tok, int64_t unit) {  // by whole units
+        return !q || (aligned(q, (size_t)unit) && (rows_seq <= 1 || seq * (int64_t)es % unit == 0) &&
+                      (pr.seqlen <= 1 || tok * (int64_t)es % unit == 0));
+    };
+    for (const int unit : {16, 8, 4})
+        if (!p.unit && rows_of(p.x, p.x_seq, p.x_tok, unit) && rows_of(p.dt, p.dt_seq, p.dt_tok, unit) &&
+            rows_of(p.z, p.z_seq, p.z_tok, unit) && rows_of(p.y, p.y_seq, p.y_tok, unit) &&
+            (pr.ngroups == 1 || cpg_bytes % unit == 0))
+            p.unit = unit;
+    ScanPlan pl = plan_scan(pr, sms, true, p.unit == 0);
+    if (workspace_bytes < pl.bytes) pl = plan_scan(pr, sms, false, false);  // too small for segments: one chain a sequence
     char *ws = static_cast<char *>(workspace);
     p.nseg = pl.nseg;
     p.seg_len = pl.seg_len;
     p.seg_items = pl.items;
     p.seg_state = reinterpret_cast<float *>(ws + pl.state_off);
     p.seg_dt = reinterpret_cast<float *>(ws + pl.dt_off);
-    const int64_t vec = 16 / (int64_t)es;  // 16-byte rows of channels
-    auto rows16 = [&](const void *q, int64_t seq, int64_t tok) {
-        return !q || (aligned(q, 16) && (rows_seq <= 1 || seq % vec == 0) && (pr.seqlen <= 1 || tok % vec == 0));
-    };
-    p.vec = rows16(p.x, p.x_seq, p.x_tok) && rows16(p.dt, p.dt_seq, p.dt_tok) && rows16(p.z, p.z_seq, p.z_tok) &&
-            rows16(p.y, p.y_seq, p.y_tok) && (pr.ngroups == 1 || p.cpg % vec == 0);
     auto states4 = [&](const void *q, int64_t seq, int64_t tok) {  // four states of B and C, or of a whole R of a step
         const size_t a = pr.dstate > 128 ? 8 * es : 4 * es;
         return aligned(q, a) && (rows_seq <= 1 || seq * es % a == 0) && (pr.seqlen <= 1 || tok * es % a == 0) &&

@@ -9,15 +9,16 @@
 // and quarter for the recurrence alone. So the states stay in registers, and what is around it is kept small:
 //
 //  - A CTA owns CT channels (of one group) and walks tokens in tiles of TT. A tile's x, dt and z are copied to shared
-//    memory one tile ahead (16-byte asynchronous copies, or through registers where rows are not 16-byte multiples); each
+//    memory one tile ahead (asynchronous copies of 16, 8 or 4 bytes as rows are aligned, or through registers); each
 //    thread turns the vectors that it copied into (dt, dt x)
 //    per token and channel, B and C are kept in fp32. The softplus is so taken once per (token, channel).
 //  - A thread holds CH channels x R states in packed pairs, S lanes share the states of its channels. A shared memory
 //    load costs its bytes per lane, broadcast or not (an LDS.128 four cycles of the SM's pipe), and B and C are eight
 //    bytes for every element: with one channel a thread they took 3.4 cycles an element and bounded the kernel. CH = 4,
-//    R = 8 (128 registers, 8 warps' worth of CTAs) and CH = 2, R = 8 (96) measure the same where segments fill the GPU
-//    (16384 x 5120 x 16: 0.70 ms); where they are not needed the smaller one has more warps (32 x 4096 x 1536 x 16: 1.28
-//    against 1.75 ms) and is taken.
+//    R = 8 (128 registers) and CH = 2, R = 8 (96) measure the same where segments fill the GPU (16384 x 5120 x 16:
+//    0.73 ms); where they are not needed the smaller one has more warps (32 x 4096 x 1536 x 16: 1.75 ms against 1.28
+//    when both were measured, now 1.48) and is taken. Up to 8 states a tile is 4 tokens and not 8, which 16 tiles an SM would not fit in shared memory
+//    (4 x 4096 x 1536 x 4: 131 us against 178; 12824 x 4000 x 8: 330 against 380).
 //  - The sum over a channel's lanes is taken for the thread's channels at once, each shuffle halving the channels a
 //    lane holds.
 //
@@ -100,8 +101,9 @@ __device__ __forceinline__ int64_t seq_at(const int32_t *cu, int64_t nseq, int64
     return n > 0 ? n - 1 : 0;  // malformed offsets may start past t
 }
 
-template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_ = 512 / NT_> struct Shape {
+template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_, int SINGLE_> struct Shape {
     static constexpr int S = S_, R = R_, CH = CH_, NT = NT_, TT = TT_, MINB = MINB_;
+    static constexpr int MINB_SINGLE = SINGLE_;  // CTAs an SM holds of the instances of UNIT 0
     static constexpr int CT = NT / S * CH, NP = S * R, CV = CT / 8;  // channels, states, 8-channel vectors of a CTA
     static constexpr int VPT = (TT * CV + NT - 1) / NT;              // vectors a thread copies per tensor
     static constexpr int NV = NP / 4;                                // 4-state vectors per token
@@ -111,10 +113,11 @@ template <int S_, int R_, int CH_, int NT_, int TT_, int MINB_ = 512 / NT_> stru
     }
 };
 
-// Without VEC (rows that are not 16-byte multiples) a tile's elements wait one by one in registers: held to the same
-// registers these instances would spill, so they keep fewer CTAs (12824 x 3981 x 8: 0.49 ms against 0.60).
-template <typename IO, typename T, bool SUM, bool VEC>
-__global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB * 3 / 4 : T::MINB - 1) scan_kernel(ScanParams p) {
+// UNIT: bytes that rows are copied by: 16, 4 (and 8; 4 x 4096 x 1540 x 16: 296 us, by single elements 371), or 0 for
+// single elements, 16-bit rows of odd widths or addresses. These wait one by one in registers: held to the same registers
+// those instances would spill, so they keep fewer CTAs (12824 x 3981 x 8: 0.49 ms against 0.60).
+template <typename IO, typename T, bool SUM, int UNIT>
+__global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_kernel(ScanParams p) {
     constexpr int S = T::S, R = T::R, NT = T::NT, TT = T::TT, CT = T::CT, NP = T::NP, CV = T::CV, VPT = T::VPT,
                   NV = T::NV, P = R / 2, kCH = T::CH;
     constexpr int BPT = (TT * NV * (SUM ? 1 : 2) + NT - 1) / NT;
@@ -198,8 +201,19 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
     auto copy = [&](IO *dst, const IO *src) {
         if (vlive == 8) {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(IO) / 2; ++i)
-                cp_async16(reinterpret_cast<uint8_t *>(dst) + 16 * i, reinterpret_cast<const uint8_t *>(src) + 16 * i);
+            for (int i = 0; i < (int)sizeof(IO) / 2; ++i) {
+                uint8_t *d = reinterpret_cast<uint8_t *>(dst) + 16 * i;
+                const uint8_t *s = reinterpret_cast<const uint8_t *>(src) + 16 * i;
+                if constexpr (UNIT == 16) {
+                    cp_async16(d, s);
+                } else if (p.unit == 8) {
+                    cp_async<8>(d, s);
+                    cp_async<8>(d + 8, s + 8);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) cp_async<4>(d + j, s + j);
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) dst[i] = i < vlive ? src[i] : from_f32<IO>(0.f);
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
     // element offsets of this thread's first vectors in the tile that is copied next, stepped from tile to tile
     int64_t ox = (t0 + trow) * p.x_tok + cv, od = (t0 + trow) * p.dt_tok + cv, oz = (t0 + trow) * p.z_tok + cv;
     const int b_t = tid / NV % TT, b_n = tid % NV * 4;
-    Raw<IO, 8> ahead[VEC ? 1 : SUM ? 2 : 3][VEC ? 1 : VPT];
+    Raw<IO, 8> ahead[UNIT ? 1 : SUM ? 2 : 3][UNIT ? 1 : VPT];
     auto load = [&](int64_t tile, int stage) {
         IO *st = raw + stage * (SUM ? 2 : 3) * RAW + trow * CT + cv;
         const int n = (int)(t1 - tile < TT ? t1 - tile : TT);
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
                 const IO *px = at(x, p.x, ox + v * TSTEP * p.x_tok, vlive, xn);
                 const IO *pd = at(dt, p.dt, od + v * TSTEP * p.dt_tok, vlive, dn);
                 const IO *pz = !SUM && z ? at(z, p.z, oz + v * TSTEP * p.z_tok, vlive, zn) : nullptr;
-                if constexpr (VEC) {
+                if constexpr (UNIT != 0) {
                     copy(st + v * TSTEP * CT, px);
                     copy(st + RAW + v * TSTEP * CT, pd);
                     if (!SUM && pz) copy(st + 2 * RAW + v * TSTEP * CT, pz);
@@ -399,7 +413,7 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (tile == t0) __syncthreads();  // bias_s and D_s
         IO *st = raw + stage * (SUM ? 2 : 3) * RAW;
-        if constexpr (!VEC) {
+        if constexpr (UNIT == 0) {
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int t = trow + v * TSTEP;
@@ -494,7 +508,7 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
                             o[i + 1] *= silu_f32(g.y);
                         }
                     IO *out = chk(static_cast<IO *>(p.y), oy + v * TSTEP * p.y_tok, vlive, yn, p.hdr, SITE_SCAN_Y);
-                    if (!VEC && vlive == 8) {
+                    if (UNIT == 0 && vlive == 8) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) out[i] = from_f32<IO>(o[i]);
                     } else if (vlive == 8) {
@@ -502,9 +516,15 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) w.set_pair(i, o[i], o[i + 1]);
 #pragma unroll
-                        for (int i = 0; i < Raw<IO, 8>::W / 4; ++i)
-                            reinterpret_cast<uint4 *>(out)[i] =
-                                make_uint4(w.w[4 * i], w.w[4 * i + 1], w.w[4 * i + 2], w.w[4 * i + 3]);
+                        for (int i = 0; i < Raw<IO, 8>::W / 4; ++i) {
+                            if constexpr (UNIT == 16) {
+                                reinterpret_cast<uint4 *>(out)[i] =
+                                    make_uint4(w.w[4 * i], w.w[4 * i + 1], w.w[4 * i + 2], w.w[4 * i + 3]);
+                            } else {
+#pragma unroll
+                                for (int j = 4 * i; j < 4 * i + 4; ++j) reinterpret_cast<uint32_t *>(out)[j] = w.w[j];
+                            }
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -530,33 +550,67 @@ __global__ void __launch_bounds__(T::NT, VEC ? T::MINB : T::MINB > 5 ? T::MINB *
 }
 
 // seg_state[i], the leaving state of segment i from a zero state -> from its true entering state (which is what enters
-// segment i + 1). A thread takes one state of a channel through the segments of a sequence (packed: of the axis).
-constexpr int kJoin = 16;
+// segment i + 1). A chain is a state of a channel through the segments of a sequence (packed: of the axis). What bounds
+// it is waiting for memory: so a thread takes kJoin segments that are all on their way at once, and up to kJoinThreads
+// threads share a chain, each first joining its own segments from a zero state (9001 x 1000 x 24: 76 segments 12 us from
+// cold memory; one thread a chain took 90 for 188).
+constexpr int kJoin = 16, kJoinThreads = 8, kJoinChains = 32;
 
-static __global__ void __launch_bounds__(256) join_kernel(ScanParams p) {
+static __global__ void __launch_bounds__(kJoinChains *kJoinThreads) join_kernel(ScanParams p) {
+    __shared__ float2 part[2][kJoinThreads][kJoinChains];  // (sum of dt, leaving state) of the threads' segments
     after_previous();
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, dn = p.D_ * p.N;
+    const int64_t e = (int64_t)blockIdx.x * kJoinChains + threadIdx.x, dn = p.D_ * p.N;
     const int64_t chains = p.cu ? 1 : p.nseq, segs = p.nseg - 1;
-    if (e >= chains * dn) return;
-    const int64_t i = e % dn, c = i / p.N, base = e / dn * segs;
-    const float a = p.A[i] * kLog2e;
+    const bool live = e < chains * dn;
+    int64_t i = 0, c = 0, base = 0, rest;
+    if (live) {
+        base = quick_div(e, dn, i) * segs;
+        c = quick_div(i, p.N, rest);
+    }
+    const float a = live ? p.A[i] * kLog2e : 0.f;
     const int64_t extent = p.seg_items * dn;
     (void)extent;
-    float h = *chk(p.seg_state, base * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
-    for (int64_t j0 = 1; j0 < segs; j0 += kJoin) {  // kJoin segments on their way at a time
+    // (d, v) leaves h as exp(a d) h + v; as v where d is NaN: a segment in which a sequence begins
+    auto pass = [&](float d, float v, float h) { return d != d ? v : fmaf(ex2(a * d), h, v); };
+    float enter = 0.f;  // the state that enters this round's segments
+    int parity = 0;
+    for (int64_t r0 = 0; r0 < segs; r0 += kJoin * blockDim.y, parity ^= 1) {
+        const int64_t j0 = r0 + threadIdx.y * kJoin;
+        const int n = !live || j0 >= segs ? 0 : (int)(segs - j0 < kJoin ? segs - j0 : kJoin);
         float v[kJoin], d[kJoin];
-        float *s = chk(p.seg_state, (base + j0) * dn + i, 1, extent, p.hdr, SITE_SCAN_SEG);
-        const float *sd = p.seg_dt + (base + j0) * p.D_ + c;
-        const int n = (int)(segs - j0 < kJoin ? segs - j0 : kJoin);
+        float *s = chk(p.seg_state, n ? (base + j0) * dn + i : 0, n ? (n - 1) * dn + 1 : 0, extent, p.hdr, SITE_SCAN_SEG);
+        const float *sd = p.seg_dt + (n ? (base + j0) * p.D_ + c : 0);
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j)
+        for (int j = 0; j < kJoin; ++j) {
+            v[j] = d[j] = 0.f;
             if (j < n) v[j] = s[j * dn], d[j] = sd[j * p.D_];
+        }
+        if (j0 == 0) d[0] = __int_as_float(0x7fffffff);
+        if (blockDim.y > 1) {
+            float h = 0.f, sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j)
-            if (j < n) {
-                h = d[j] != d[j] ? v[j] : fmaf(ex2(a * d[j]), h, v[j]);
-                s[j * dn] = h;
+            for (int j = 0; j < kJoin; ++j) {
+                if (j < n) h = pass(d[j], v[j], h);
+                sum += d[j];
             }
+            part[parity][threadIdx.y][threadIdx.x] = make_float2(sum, h);
+            __syncthreads();
+            float all = enter, mine = enter;
+            for (int y = 0; y < (int)blockDim.y && r0 + y * kJoin < segs; ++y) {
+                if (y == (int)threadIdx.y) mine = all;
+                const float2 w = part[parity][y][threadIdx.x];
+                all = pass(w.x, w.y, all);
+            }
+            enter = all;
+            h = mine;
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j)
+                if (j < n) s[j * dn] = h = pass(d[j], v[j], h);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j)
+                if (j < n) s[j * dn] = enter = pass(d[j], v[j], enter);
+        }
     }
 }
 
@@ -703,34 +757,47 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
         body(std::integral_constant<bool, false>());
 }
 
-template <typename IO, typename T, bool SUM, bool VEC>
+template <typename IO, typename T, bool SUM, int UNIT>
 cudaError_t launch_pass(const ScanParams &p, int64_t items, cudaStream_t stream) {
     const int64_t grid = items * ((p.cpg + T::CT - 1) / T::CT) * p.G;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    auto k = scan_kernel<IO, T, SUM, VEC>;
+    auto k = scan_kernel<IO, T, SUM, UNIT>;
     constexpr size_t smem = T::smem(SUM, sizeof(IO));
-    if (smem > 48 * 1024) {
+    if constexpr (smem > 48 * 1024) {
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = allow_smem(k, smem, done);
         if (e != cudaSuccess) return e;
     }
+    if (p.nseg == 1) {
+        // Whole chains, fewer CTAs than fit, start once the kernel before has left every SM: started as its CTAs leave,
+        // they crowd on the SMs that come free first (32 x 4096 x 1536 x 16, 384 CTAs: 2.00 ms against 1.48).
+        k<<<(unsigned)grid, T::NT, smem, stream>>>(p);
+        return cudaGetLastError();
+    }
     return launch_after(k, grid, T::NT, smem, stream, p);
+}
+template <typename IO, typename T, bool SUM>
+cudaError_t launch_rows(const ScanParams &p, int64_t items, cudaStream_t stream) {
+    if constexpr (sizeof(IO) < 4)
+        if (p.unit == 0) return launch_pass<IO, T, SUM, 0>(p, items, stream);
+    return p.unit == 16 ? launch_pass<IO, T, SUM, 16>(p, items, stream) : launch_pass<IO, T, SUM, 4>(p, items, stream);
 }
 template <typename IO, typename T>
 cudaError_t launch_shape(const ScanParams &p, cudaStream_t stream) {
     if (p.nseg > 1) {
-        cudaError_t e = p.vec ? launch_pass<IO, T, true, true>(p, p.seg_items, stream)
-                              : launch_pass<IO, T, true, false>(p, p.seg_items, stream);
+        cudaError_t e = launch_rows<IO, T, true>(p, p.seg_items, stream);
         if (e != cudaSuccess) return e;
         if (p.nseg > 2) {
-            const int64_t grid = ((p.cu ? 1 : p.nseq) * p.D_ * p.N + 255) / 256;
+            const int64_t grid = ((p.cu ? 1 : p.nseq) * p.D_ * p.N + kJoinChains - 1) / kJoinChains;
             if (grid > INT32_MAX) return cudaErrorInvalidValue;
-            e = launch_after(join_kernel, grid, 256, 0, stream, p);
+            const int64_t share = (p.nseg - 1 + kJoin - 1) / kJoin;
+            e = launch_after(join_kernel, grid, dim3(kJoinChains, (unsigned)std::min<int64_t>(share, kJoinThreads)), 0,
+                             stream, p);
             if (e != cudaSuccess) return e;
         }
     }
     const int64_t items = p.cu ? p.nseg : p.nseq * p.nseg;
-    return p.vec ? launch_pass<IO, T, false, true>(p, items, stream) : launch_pass<IO, T, false, false>(p, items, stream);
+    return launch_rows<IO, T, false>(p, items, stream);
 }
 template <typename IO, int S, int R>
 cudaError_t launch_step_kernel(const ScanParams &p, cudaStream_t stream) {
@@ -742,18 +809,20 @@ cudaError_t launch_step_kernel(const ScanParams &p, cudaStream_t stream) {
 }
 
 // By the number of states; scan_cta (ssd_internal.h) tells the planner their channels and threads.
-using Shape4 = Shape<1, 4, 4, 32, 8, 16>;
-using Shape8 = Shape<1, 8, 2, 64, 8, 10>;
-using Shape16 = Shape<2, 8, 2, 128, 8, 5>;
-using Shape24 = Shape<2, 12, 2, 128, 8, 4>;
-using Shape32 = Shape<4, 8, 2, 256, 8, 2>;
-using Shape64 = Shape<8, 8, 2, 256, 8, 2>;
-using Shape128 = Shape<16, 8, 2, 256, 8, 2>;
-using Shape256 = Shape<32, 8, 2, 256, 8, 2>;
+using Shape4 = Shape<1, 4, 4, 32, 4, 16, 12>;
+using Shape8 = Shape<1, 8, 2, 64, 4, 8, 7>;
+using Shape16 = Shape<2, 8, 2, 128, 8, 5, 4>;
+using Shape24 = Shape<2, 12, 2, 128, 8, 4, 3>;
+using Shape32 = Shape<4, 8, 2, 256, 8, 2, 1>;
+using Shape64 = Shape<8, 8, 2, 256, 8, 2, 1>;
+using Shape128 = Shape<16, 8, 2, 256, 8, 2, 1>;
+using Shape256 = Shape<32, 8, 2, 256, 8, 2, 1>;
 
 template <typename IO, typename T> cudaError_t launch_checked(const ScanParams &p, cudaStream_t stream) {
     const ScanCta c = scan_cta(p.N);
-    return c.channels == T::CT && c.threads == T::NT && c.resident == T::MINB * T::NT ? launch_shape<IO, T>(p, stream) : cudaErrorInvalidValue;
+    const bool agree = c.channels == T::CT && c.threads == T::NT && c.resident == T::MINB &&
+                       c.resident_single == T::MINB_SINGLE;
+    return agree ? launch_shape<IO, T>(p, stream) : cudaErrorInvalidValue;
 }
 
 template <typename IO> cudaError_t launch_io(const ScanParams &p, cudaStream_t stream) {
