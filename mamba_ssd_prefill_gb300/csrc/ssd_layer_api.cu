@@ -60,16 +60,17 @@ ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments, bool sin
     // Without segments the work of a chain runs once, with them its states' part twice. So segments are cut only where
     // the CTAs leave the SMs short of warps (under about 1.3 CTAs of 128 threads each: 4 x 4096 x 1536 x 16, 48 CTAs,
     // 0.84 ms in one chain and 0.24 segmented; 32 x 4096 x 1536 x 16, 384 CTAs, 1.28 and 1.57 ms when both were
-    // measured), and then so many that
-    // the resident CTAs are full once, or twice where segments are long: a part of a wave leaves SMs idle (8192 x 5120 x
-    // 16: 0.5, 1, 1.5 and 2 waves 0.70, 0.378, 0.416 and 0.379 ms; 16384 x 5120 x 16: 1 and 2 waves 0.736 and 0.728), and
-    // more segments pay their entry more often (4000 x 1536 x 16, packed: 1 and 2 waves 75 and 85 us).
+    // measured), and then so many that the resident CTAs are full once, or twice where segments are long: a part of a
+    // wave leaves SMs idle (8192 x 5120 x 16: 0.5, 1, 1.5 and 2 waves 0.70, 0.378, 0.416 and 0.379 ms; 16384 x 5120 x 16:
+    // 1 and 2 waves 0.736 and 0.728), and more segments pay their entry more often (4000 x 1536 x 16, packed: 1 and 2
+    // waves 75 and 85 us).
     const ssd::ScanCta cta = ssd::scan_cta(p.dstate);
     const int64_t per_group = (p.channels / p.ngroups + cta.channels - 1) / cta.channels;
     const int64_t ctas = chains * p.ngroups * per_group, threads = ctas * cta.threads;
     if (threads * 10 >= 13 * 128 * (int64_t)sms) return pl;
+    const int64_t waves = p.seqlen >= 2 * 400 * (cta.resident * (int64_t)sms / ctas) ? 2 : 1;  // the same for single
     const int64_t wave = (int64_t)(single ? cta.resident_single : cta.resident) * sms / ctas;
-    const int64_t want = std::min<int64_t>(p.seqlen >= 2 * wave * 400 ? 2 * wave : wave, p.seqlen / 16);
+    const int64_t want = std::min<int64_t>(waves * wave, p.seqlen / 16);
     if (want < 2) return pl;
     int64_t len = (p.seqlen + want - 1) / want;
     len = (len + 7) / 8 * 8;  // whole tiles
