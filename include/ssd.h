@@ -354,7 +354,7 @@ typedef struct {
     const void *dt_raw;       /* as x                                          */
     const void *z;            /* as x, or NULL: no gate                        */
     const void *B, *C;        /* [batch, seqlen, ngroups, dstate], a token's G*N contiguous */
-    void *y;                  /* as x                                          */
+    void *y;                  /* as x; must not overlap the inputs             */
     const float *A;           /* [channels, dstate] contiguous                 */
     const float *dt_bias;     /* [channels] or NULL                            */
     const float *D;           /* [channels] or NULL                            */
