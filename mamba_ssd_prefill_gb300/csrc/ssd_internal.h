@@ -138,8 +138,9 @@ struct RowConvParams {
     int64_t nseq, L, T, D;
     int64_t x_seq, x_tok, out_seq, out_tok;
     int k, silu;
-    int vec, vec_state, vec_w;  // rows of x and out, the cache left behind, and the taps lie on 16-byte boundaries
-    int64_t rows;               // leading dimension of x and out (packed: 1)
+    int unit;              // bytes that rows of x and out are copied by: 16, 4, or 0 (single elements)
+    int vec_state, vec_w;  // the cache left behind, and the taps lie on 16-byte boundaries
+    int64_t rows;          // leading dimension of x and out (packed: 1)
 };
 cudaError_t launch_row_conv(const RowConvParams &p, int io_dtype, int sms, cudaStream_t stream);
 

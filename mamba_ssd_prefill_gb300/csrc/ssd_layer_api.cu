@@ -271,11 +271,14 @@ SSD_API ssd_status_t ssd_conv(const ssd_conv_problem_t *prob, const ssd_conv_ten
     p.k = pr.width;
     p.silu = pr.activation == SSD_ACT_SILU;
     p.rows = rows_seq;
-    const int64_t vec = 16 / (int64_t)es;
-    auto rows16 = [&](const void *q, int64_t seq, int64_t tok) {
-        return aligned(q, 16) && (rows_seq <= 1 || seq % vec == 0) && (pr.seqlen <= 1 || tok % vec == 0);
+    auto rows_of = [&](const void *q, int64_t seq, int64_t tok, int64_t unit) {  // by whole units
+        return aligned(q, (size_t)unit) && (rows_seq <= 1 || seq * (int64_t)es % unit == 0) &&
+               (pr.seqlen <= 1 || tok * (int64_t)es % unit == 0);
     };
-    p.vec = pr.channels % vec == 0 && rows16(p.x, p.x_seq, p.x_tok) && rows16(p.out, p.out_seq, p.out_tok);
+    for (const int unit : {16, 4})
+        if (!p.unit && pr.channels * (int64_t)es % unit == 0 && rows_of(p.x, p.x_seq, p.x_tok, unit) &&
+            rows_of(p.out, p.out_seq, p.out_tok, unit))
+            p.unit = unit;
     p.vec_state = aligned(p.state_out, 16) && aligned(p.state, 16);
     p.vec_w = aligned(p.w, 16);
     return ssd::launch_row_conv(p, pr.io_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK

@@ -8,7 +8,8 @@
 // other thread touches: 32 KB a CTA in flight without a register or a barrier (loads to registers, eight ahead, kept
 // 168 registers and 12 warps and ran 8 x 8192 x 5376 channels in 396 us; the ring with a predicate on every token 361;
 // whole stages without one, so that the window of inputs is renamed and not moved, 216 us, 6.5 TB/s). Rows that are
-// not 16-byte multiples take one channel a thread from registers (5377 channels: 374 us).
+// not 16-byte multiples are copied in units of 4 bytes (5378 channels: 296 us); 16-bit rows of odd widths or addresses
+// take one channel a thread from registers (5377 channels: 399 us).
 // The cache leaves with the thread that walks a sequence's last token, so a prompt takes one launch, and a single token
 // too: its thread reads the old cache before it writes the new one. Only where the cache is updated in place and another
 // thread reads its old entries does a second kernel write it.
@@ -66,22 +67,27 @@ __device__ __forceinline__ void next_sequence(const RowConvParams &p, Walk &w, i
     if (w.s >= p.nseq) w.s = p.nseq - 1, w.start = t, w.end = p.T + 1;  // malformed offsets
 }
 
-// V channels a thread (16 bytes; V = 1: rows that are not 16-byte multiples). The rows come through a ring in shared
+// V channels a thread (16 bytes; V = 1: single elements), rows copied by UNIT bytes (16 or 4). The rows come through a ring in shared
 // memory, kGroup tokens a stage, in slots that only their thread writes and reads (no barrier); V = 1 loads a stage's
 // tokens to registers instead.
+// CTAs an SM: by registers; with more the wider windows spill (8 x 8192 x 5376, width 5: 4 CTAs 279 us, 3 268; width 8: 3
+// 506, 2 464; width 7: 3 339, 2 378).
 constexpr int kStages = 4;
 
-template <typename IO, int K, int V>
-__global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
+template <typename IO, int K, int V, int UNIT>
+__global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 7 ? 2 : K > 4 ? 3 : 4)
     row_conv_kernel(RowConvParams p, int tl, int64_t tiles, int write_state) {
     constexpr int KH = K > 1 ? K - 1 : 1, P = V > 1 ? V / 2 : 1, G = V > 1 ? 4 : 8;  // P: channel pairs, G: tokens a stage
     __shared__ uint4 ring[V > 1 ? kStages * G : 1][V > 1 ? kThreads : 1];
-    const int64_t nvec = p.D / V, idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    constexpr bool PART = V > 1 && UNIT < 16;       // a row's last thread may hold fewer channels
+    constexpr int E = 4 / (int)sizeof(IO);          // elements of 4 bytes
+    const int64_t nvec = (p.D + V - 1) / V, idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     after_previous();
     if (p.cu && blockIdx.x == 0) check_offsets(p.cu, p.nseq, p.T, p.hdr);
     int64_t cvec;
     const int64_t item = quick_div(idx, nvec, cvec), c = cvec * V;
     if (item >= (p.cu ? tiles : p.nseq * tiles)) return;
+    const int live = PART && p.D - c < V ? (int)(p.D - c) : V;
     Walk wk = walk_of(p, item, tiles, tl);
     const IO *x = static_cast<const IO *>(p.x);
     const IO *state = static_cast<const IO *>(p.state);
@@ -97,9 +103,17 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
         if constexpr (V > 1) {
 #pragma unroll
             for (int u = 0; u < G; ++u)
-                if (fetched + u < wk.t1)
-                    cp_async16(&ring[stage * G + u][threadIdx.x],
-                               chk(x, xt + u * p.x_tok, V, xn, p.hdr, SITE_RCONV_IN));
+                if (fetched + u < wk.t1) {
+                    const IO *s = chk(x, xt + u * p.x_tok, live, xn, p.hdr, SITE_RCONV_IN);
+                    uint4 *d = &ring[stage * G + u][threadIdx.x];
+                    if constexpr (PART) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j * E < live) cp_async<4>(reinterpret_cast<uint32_t *>(d) + j, s + j * E);
+                    } else {
+                        cp_async16(d, s);
+                    }
+                }
             asm volatile("cp.async.commit_group;" ::: "memory");
             xt += G * p.x_tok;
             fetched += G;
@@ -111,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
     float2 hist[KH][P];  // hist[j]: the input of token t - 1 - j (V = 1: its .x)
     // inputs before token t of sequence q on [begin, ..)
     auto load_hist = [&](int64_t q, int64_t t, int64_t begin) {
-        if (V > 1 && K > 1 && t == begin && state && p.vec_state) {  // all of them cached: whole vectors
+        if (V > 1 && !PART && K > 1 && t == begin && state && p.vec_state) {  // all of them cached: whole vectors
             Raw<IO, V * KH> r;
             r.load(chk(state, (q * p.D + c) * (K - 1), V * (K - 1), sn, p.hdr, SITE_RCONV_STATE));
 #pragma unroll
@@ -126,13 +140,13 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
             const int64_t tp = t - 1 - j;
             float v[2 * P];
             if (tp >= begin) {
-                const IO *r = chk(x, xo + tp * p.x_tok, V, xn, p.hdr, SITE_RCONV_IN);
+                const IO *r = chk(x, xo + tp * p.x_tok, live, xn, p.hdr, SITE_RCONV_IN);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = to_f32(r[i]);
+                for (int i = 0; i < V; ++i) v[i] = i < live ? to_f32(r[i]) : 0.f;
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    v[i] = state ? to_f32(*chk(state, (q * p.D + c + i) * (K - 1) + (K - 1) + (tp - begin), 1, sn,
+                    v[i] = state && i < live ? to_f32(*chk(state, (q * p.D + c + i) * (K - 1) + (K - 1) + (tp - begin), 1, sn,
                                                p.hdr, SITE_RCONV_STATE))
                                  : 0.f;
             }
@@ -149,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
                     v[i * KH + j] = from_f32<IO>(i % 2 ? hist[K - 2 - j][i / 2].y : hist[K - 2 - j][i / 2].x);
-            IO *o = chk(sout, (q * p.D + c) * (K - 1), V * (K - 1), sn, p.hdr, SITE_RCONV_STATE);
-            if (V > 1 && p.vec_state) {
+            IO *o = chk(sout, (q * p.D + c) * (K - 1), live * (K - 1), sn, p.hdr, SITE_RCONV_STATE);
+            if (V > 1 && !PART && p.vec_state) {
 #pragma unroll
                 for (int i = 0; i < V * KH * (int)sizeof(IO) / 16; ++i) {
                     uint4 u;
@@ -159,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < V * KH; ++i) o[i] = v[i];
+                for (int i = 0; i < V * KH; ++i)
+                    if (i < live * KH) o[i] = v[i];
             }
         }
     };
@@ -174,19 +189,20 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float t[K];
+        const int64_t ci = i < live ? c + i : c;
         if constexpr (K == 4) {
             if (p.vec_w) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(p.w + (c + i) * 4));
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(p.w + ci * 4));
                 t[0] = u.x, t[1] = u.y, t[2] = u.z, t[3] = u.w;
             } else {
 #pragma unroll
-                for (int j = 0; j < K; ++j) t[j] = p.w[(c + i) * K + j];
+                for (int j = 0; j < K; ++j) t[j] = p.w[ci * K + j];
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < K; ++j) t[j] = p.w[(c + i) * K + j];
+            for (int j = 0; j < K; ++j) t[j] = p.w[ci * K + j];
         }
-        const float b = p.bias ? p.bias[c + i] : 0.f;
+        const float b = p.bias ? p.bias[ci] : 0.f;
 #pragma unroll
         for (int j = 0; j < K; ++j)
             if (i % 2) w[j][i / 2].y = t[j];
@@ -217,12 +233,18 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 5 ? 3 : 4)
                 if (V > 1) acc[i].y = silu_f32(acc[i].y);
             }
         }
-        IO *dst = chk(out, oo + u * p.out_tok, V, on, p.hdr, SITE_RCONV_OUT);
+        IO *dst = chk(out, oo + u * p.out_tok, live, on, p.hdr, SITE_RCONV_OUT);
         if constexpr (V > 1) {
             Raw<IO, V> o;
 #pragma unroll
             for (int i = 0; i < P; ++i) o.set_pair(2 * i, acc[i].x, acc[i].y);
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+            if constexpr (PART) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j * E < live) reinterpret_cast<uint32_t *>(dst)[j] = o.w[j];
+            } else {
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+            }
         } else {
             *dst = from_f32<IO>(acc[0].x);
         }
@@ -329,23 +351,23 @@ __global__ void __launch_bounds__(kThreads) row_conv_state_kernel(RowConvParams 
     }
 }
 
-template <typename IO, int K, int V>
+template <typename IO, int K, int V, int UNIT>
 cudaError_t launch_kv(const RowConvParams &p, int tl, int64_t tiles, int write_state, cudaStream_t stream) {
-    const int64_t threads = (p.cu ? tiles : p.nseq * tiles) * (p.D / V), grid = (threads + kThreads - 1) / kThreads;
+    const int64_t threads = (p.cu ? tiles : p.nseq * tiles) * ((p.D + V - 1) / V), grid = (threads + kThreads - 1) / kThreads;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_after(row_conv_kernel<IO, K, V>, grid, kThreads, 0, stream, p, tl, tiles, write_state);
+    return launch_after(row_conv_kernel<IO, K, V, UNIT>, grid, kThreads, 0, stream, p, tl, tiles, write_state);
 }
-template <typename IO, int V>
+template <typename IO, int V, int UNIT>
 cudaError_t launch_v(const RowConvParams &p, int tl, int64_t tiles, int write_state, cudaStream_t stream) {
     switch (p.k) {
-        case 1: return launch_kv<IO, 1, V>(p, tl, tiles, write_state, stream);
-        case 2: return launch_kv<IO, 2, V>(p, tl, tiles, write_state, stream);
-        case 3: return launch_kv<IO, 3, V>(p, tl, tiles, write_state, stream);
-        case 4: return launch_kv<IO, 4, V>(p, tl, tiles, write_state, stream);
-        case 5: return launch_kv<IO, 5, V>(p, tl, tiles, write_state, stream);
-        case 6: return launch_kv<IO, 6, V>(p, tl, tiles, write_state, stream);
-        case 7: return launch_kv<IO, 7, V>(p, tl, tiles, write_state, stream);
-        default: return launch_kv<IO, 8, V>(p, tl, tiles, write_state, stream);
+        case 1: return launch_kv<IO, 1, V, UNIT>(p, tl, tiles, write_state, stream);
+        case 2: return launch_kv<IO, 2, V, UNIT>(p, tl, tiles, write_state, stream);
+        case 3: return launch_kv<IO, 3, V, UNIT>(p, tl, tiles, write_state, stream);
+        case 4: return launch_kv<IO, 4, V, UNIT>(p, tl, tiles, write_state, stream);
+        case 5: return launch_kv<IO, 5, V, UNIT>(p, tl, tiles, write_state, stream);
+        case 6: return launch_kv<IO, 6, V, UNIT>(p, tl, tiles, write_state, stream);
+        case 7: return launch_kv<IO, 7, V, UNIT>(p, tl, tiles, write_state, stream);
+        default: return launch_kv<IO, 8, V, UNIT>(p, tl, tiles, write_state, stream);
     }
 }
 
@@ -354,7 +376,8 @@ cudaError_t launch_t(const RowConvParams &p, int sms, cudaStream_t stream) {
     const size_t state_bytes = (size_t)(p.nseq * p.D * (p.k - 1)) * sizeof(IO);
     bool save_after = p.state_out && p.k > 1 && p.T == 0;
     if (p.T > 0) {
-        const int64_t V = p.vec ? 16 / (int64_t)sizeof(IO) : 1, L = p.cu ? p.T : p.L, chains = p.cu ? 1 : p.nseq;
+        constexpr int kVec = 16 / (int)sizeof(IO);
+        const int64_t V = p.unit ? kVec : 1, L = p.cu ? p.T : p.L, chains = p.cu ? 1 : p.nseq;
         // 64 tokens a thread (8 x 8192 x 5376: 16 tokens 326 us, 32 240, 64 216, 256 234); shorter walks where those leave
         // SMs idle (4096 x 5376: 32 and 64 tokens 23.5 us, 128 31)
         int tl = 64;
@@ -364,8 +387,11 @@ cudaError_t launch_t(const RowConvParams &p, int sms, cudaStream_t stream) {
         const bool shared = a && b && a < b + state_bytes && b < a + state_bytes;
         save_after = p.state_out && p.k > 1 && shared && (tiles > 1 || p.cu || a != b);
         const int write_state = p.state_out && p.k > 1 && !save_after;
-        const cudaError_t e = p.vec ? launch_v<IO, 16 / (int)sizeof(IO)>(p, tl, tiles, write_state, stream)
-                                    : launch_v<IO, 1>(p, tl, tiles, write_state, stream);
+        cudaError_t e;
+        if (p.unit == 16) e = launch_v<IO, kVec, 16>(p, tl, tiles, write_state, stream);
+        else if (p.unit == 4) e = launch_v<IO, kVec, 4>(p, tl, tiles, write_state, stream);
+        else if constexpr (sizeof(IO) < 4) e = launch_v<IO, 1, 0>(p, tl, tiles, write_state, stream);
+        else e = cudaErrorInvalidValue;
         if (e != cudaSuccess) return e;
     }
     if (save_after) {

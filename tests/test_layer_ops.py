@@ -301,6 +301,8 @@ CONV = [
     (1, 50, 24, 6, {}), (1, 50, 24, 7, dict(io=F32)),
     (1, 76, 40, 4, dict(lengths=[33, 1, 0, 2, 40])), (1, 9, 64, 8, dict(lengths=[1] * 9)),
     (1, 300, 66, 4, dict(lengths=[0, 128, 0, 3, 169, 0], io=F16)), (1, 64, 8, 4, dict(lengths=[64], state=False)),
+    (2, 140, 1030, 4, {}), (1, 90, 258, 2, dict(io=F16)), (2, 77, 5, 8, dict(io=F32)), (3, 1, 35, 4, dict(io=F32)),
+    (1, 200, 131, 3, dict(lengths=[1, 150, 0, 49], io=F32)), (1, 200, 130, 5, dict(lengths=[64, 64, 72])),
 ]
 
 
@@ -325,7 +327,7 @@ def test_conv_state_in_place(L, lengths):
 
 
 @gpu
-@pytest.mark.parametrize("off", [0, 1, 8])
+@pytest.mark.parametrize("off", [0, 1, 2, 8])
 def test_conv_slices_and_strided_output(off):
     x, w, bias, state, _ = conv_inputs(2, 45, 72, 4, seed=4)
     out0, c0 = m.ssd_conv(x, w, bias, state)
