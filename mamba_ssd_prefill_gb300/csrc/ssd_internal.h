@@ -152,7 +152,7 @@ struct NormParams {
     WsHeader *hdr;  // may be null
     int64_t rows, D, G, x_row, z_row, y_row;
     int center, gate_first, silu;
-    int vec;  // 16-byte pieces of every group of x, z, y, w and bias are aligned
+    int unit;  // bytes of the aligned pieces that every group of x, z and y is made of: 16, 4 (16-bit types), or 0
     float eps;
 };
 // ssd_norm.cuh, one translation unit per type

@@ -91,6 +91,8 @@ template <typename IO, int K> struct Raw {
     __device__ __forceinline__ void load(const IO *p) {
         if constexpr (K == 1) {
             w[0] = bits(*p);
+        } else if constexpr (W == 1) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
         } else if constexpr (W == 2) {
             const uint2 v = *reinterpret_cast<const uint2 *>(p);
             w[0] = v.x, w[1] = v.y;

@@ -327,9 +327,12 @@ SSD_API ssd_status_t ssd_group_norm(const ssd_norm_problem_t *prob, const ssd_no
     p.gate_first = pr.gate_first;
     p.silu = pr.activation == SSD_ACT_SILU;
     p.eps = pr.eps;
-    const int64_t vec = 16 / (int64_t)es, gs = pr.channels / pr.ngroups;  // 16-byte pieces of every group
-    p.vec = gs % vec == 0 && aligned(p.x, 16) && aligned(p.z, 16) && aligned(p.y, 16) && aligned(p.w, 16) &&
-            aligned(p.bias, 16) && (pr.rows == 1 || (p.x_row % vec == 0 && p.z_row % vec == 0 && p.y_row % vec == 0));
+    const int64_t vec = 16 / (int64_t)es, gs = pr.channels / pr.ngroups;
+    auto by = [&](int64_t n, size_t unit, size_t weights) {  // every group is made of pieces of n elements
+        return gs % n == 0 && aligned(p.x, unit) && aligned(p.z, unit) && aligned(p.y, unit) && aligned(p.w, weights) &&
+               aligned(p.bias, weights) && (pr.rows == 1 || (p.x_row % n == 0 && p.z_row % n == 0 && p.y_row % n == 0));
+    };
+    p.unit = by(vec, 16, 16) ? 16 : es == 2 && by(2, 4, 8) ? 4 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = pr.io_dtype == SSD_F32    ? ssd::launch_norm_f32(p, sms, s)
                           : pr.io_dtype == SSD_BF16 ? ssd::launch_norm_bf16(p, sms, s)

@@ -6,8 +6,8 @@
 // next token's vectors are loaded under the sums of this one: without that 16384 x 1536 channels with a gate took 39 us
 // however many warps there were, with it 28; four or more vectors a lane leave too few warps (39 us). In e4m3 the 16
 // (fp32: 32) lanes that hold 128 channels find their largest magnitude by shuffles. Rows that are not 16-byte multiples
-// go by single elements. Longer groups (over 24576 channels, in fp32 12288, by elements 8192), and e4m3 of unaligned rows, take the
-// kernel that reads a group three times.
+// go by pairs (16384 x 1538: 57 us) or single elements (1537: 112). Longer groups (over 24576 channels, in fp32 12288, by
+// pairs and elements 8192), and e4m3 of unaligned rows, take the kernel that reads a group three times.
 #pragma once
 
 #include "ssd_internal.h"
@@ -131,7 +131,7 @@ constexpr int kMostWarps = 16;
 enum Gate { kNone, kFirst, kAfter };
 
 // W warps a group: W = 1, four groups in a CTA of 128 threads; else one, in a CTA of 32 W threads. V: elements of a
-// vector (16 bytes, or 1); a lane's values are in packed pairs, of one vector or (V = 1) of neighbouring single elements.
+// vector (16 bytes, 4 bytes of 16-bit types, or 1); a lane's values are in packed pairs, of one vector or (V = 1) of neighbouring single elements.
 template <typename IO, int V, int NV, bool Q, int GATE>
 __global__ void __launch_bounds__(32 * kMostWarps, 1) norm_kernel(NormParams p, int W) {
     constexpr int P = NV * V / 2, PV = V / 2;  // pairs of a lane, of a vector
@@ -221,6 +221,9 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) norm_kernel(NormParams p, 
             if constexpr (V == 1) {
                 if (p.w) o[0].x *= __ldg(wp);
                 if (p.bias) o[0].x += __ldg(bp);
+            } else if constexpr (V == 2) {
+                if (p.w) o[0] = mul2(o[0], __ldg(reinterpret_cast<const float2 *>(wp)));
+                if (p.bias) o[0] = add2(o[0], __ldg(reinterpret_cast<const float2 *>(bp)));
             } else {
                 if (p.w)
 #pragma unroll
@@ -270,8 +273,9 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) norm_kernel(NormParams p, 
                         Raw<IO, V> t;
 #pragma unroll
                         for (int k = 0; k < PV; ++k) t.set_pair(2 * k, o[k].x, o[k].y);
-                        *reinterpret_cast<uint4 *>(chk(static_cast<IO *>(p.y), yi + i * apart * V, V, yn, p.hdr,
-                                                       SITE_NORM_OUT)) = make_uint4(t.w[0], t.w[1], t.w[2], t.w[3]);
+                        IO *y = chk(static_cast<IO *>(p.y), yi + i * apart * V, V, yn, p.hdr, SITE_NORM_OUT);
+                        if constexpr (V == 2) *reinterpret_cast<uint32_t *>(y) = t.w[0];
+                        else *reinterpret_cast<uint4 *>(y) = make_uint4(t.w[0], t.w[1], t.w[2], t.w[3]);
                     }
                 } else {
                     constexpr int LANES = 128 / V;  // lanes of a block; lanes past the group hold zeros
@@ -310,7 +314,7 @@ cudaError_t launch_gate(const NormParams &p, int W, int sms, cudaStream_t stream
     const int threads = W == 1 ? 128 : 32 * W;
     const int64_t items = p.rows * p.G, ctas = W == 1 ? (items + 3) / 4 : items;
     // 512 threads an SM (by elements 1024): more of them, where they fit, ran the same or slower
-    const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, (V > 1 ? 512 : 1024) / threads));
+    const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, (V > 2 ? 512 : 1024) / threads));
     if (grid == ctas) return launch_after(norm_kernel<IO, V, NV, Q, GATE>, grid, threads, 0, stream, p, W);
     // CTAs that walk rows start once the kernel before has left every SM: started as its CTAs leave, more than their
     // share would gather on the SMs that come free first (8191 x 5120 and the product behind it: 172 us against 160)
@@ -325,7 +329,7 @@ cudaError_t launch_q(const NormParams &p, int W, int sms, cudaStream_t stream) {
 }
 template <typename IO, int V, int NV>
 cudaError_t launch_nv(const NormParams &p, int W, int sms, cudaStream_t stream) {
-    if constexpr (V > 1)
+    if constexpr (V > 2)
         if (p.scales) return launch_q<IO, V, NV, true>(p, W, sms, stream);
     return launch_q<IO, V, NV, false>(p, W, sms, stream);
 }
@@ -333,18 +337,22 @@ cudaError_t launch_nv(const NormParams &p, int W, int sms, cudaStream_t stream) 
 template <typename IO> cudaError_t launch_io(const NormParams &p, int sms, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(IO);
     const int64_t gs = p.D / p.G;
-    // a CTA holds 16 warps at most, a lane up to 3 vectors (6 of longer groups), or 4 single elements (16)
-    const int64_t nvec = p.vec ? gs / V : gs;
-    if (nvec <= kMostWarps * 32 * (p.vec ? 6 : 16) && (p.vec || !p.scales)) {
-        const int few = p.vec ? 3 : 4, most = nvec <= kMostWarps * 32 * few ? few : p.vec ? 6 : 16;
+    // a CTA holds 16 warps at most, a lane up to 3 vectors (6 of longer groups), or 4 pairs (8) or single elements (16)
+    const int64_t nvec = p.unit == 16 ? gs / V : p.unit == 4 ? gs / 2 : gs;
+    const int few = p.unit == 16 ? 3 : 4, many = p.unit == 16 ? 6 : p.unit == 4 ? 8 : 16;
+    if (nvec <= kMostWarps * 32 * many && (p.unit == 16 || !p.scales)) {
+        const int most = nvec <= kMostWarps * 32 * few ? few : many;
         const int W = (int)((nvec + 32 * most - 1) / (32 * most));
         const int NV = (int)((nvec + 32 * W - 1) / (32 * W));
-        if (p.vec) switch (NV) {
+        if (p.unit == 16) switch (NV) {
             case 1: return launch_nv<IO, V, 1>(p, W, sms, stream);
             case 2: return launch_nv<IO, V, 2>(p, W, sms, stream);
             case 3: return launch_nv<IO, V, 3>(p, W, sms, stream);
             default: return launch_nv<IO, V, 6>(p, W, sms, stream);
         }
+        if constexpr (sizeof(IO) == 2)
+            if (p.unit == 4)
+                return NV <= 4 ? launch_nv<IO, 2, 4>(p, W, sms, stream) : launch_nv<IO, 2, 8>(p, W, sms, stream);
         return NV <= 4 ? launch_nv<IO, 1, 4>(p, W, sms, stream) : launch_nv<IO, 1, 16>(p, W, sms, stream);
     }
     const int64_t grid = std::min<int64_t>(p.rows * p.G, (int64_t)sms * 64);

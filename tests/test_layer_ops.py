@@ -391,7 +391,7 @@ NORM = [
     # rows, channels, groups, io
     (1, 1536, 1, BF16), (7, 1536, 24, BF16), (33, 5120, 8, BF16), (5, 200, 8, F32), (3, 1, 1, F32), (4, 7, 7, F16),
     (9, 130, 2, F16), (2, 8192, 1, F32), (3, 20000, 1, BF16), (2, 1000, 1, F16), (300, 64, 1, BF16), (65, 96, 3, F32),
-    (2, 33000, 2, BF16),
+    (2, 33000, 2, BF16), (700, 1538, 1, BF16), (9, 300, 10, F16), (3, 8190, 1, BF16), (2, 9006, 1, F16), (5, 2, 1, BF16),
 ]
 MODES = [dict(), dict(z=True), dict(z=True, gate_first=True), dict(center=True, activation="none"),
          dict(z=True, center=True), dict(z=True, gate_first=True, center=True), dict(plain=True)]
