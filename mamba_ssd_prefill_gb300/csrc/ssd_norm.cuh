@@ -6,7 +6,7 @@
 // next token's vectors are loaded under the sums of this one: without that 16384 x 1536 channels with a gate took 39 us
 // however many warps there were, with it 28; four or more vectors a lane leave too few warps (39 us). In e4m3 the 16
 // (fp32: 32) lanes that hold 128 channels find their largest magnitude by shuffles. Rows that are not 16-byte multiples
-// go by pairs (16384 x 1538: 57 us) or single elements (1537: 112). Longer groups (over 24576 channels, in fp32 12288, by
+// go by pairs (16384 x 1538: 57 us) or single elements (1537: 84). Longer groups (over 24576 channels, in fp32 12288, by
 // pairs and elements 8192), and e4m3 of unaligned rows, take the kernel that reads a group three times.
 #pragma once
 
@@ -313,8 +313,8 @@ template <typename IO, int V, int NV, bool Q, int GATE>
 cudaError_t launch_gate(const NormParams &p, int W, int sms, cudaStream_t stream) {
     const int threads = W == 1 ? 128 : 32 * W;
     const int64_t items = p.rows * p.G, ctas = W == 1 ? (items + 3) / 4 : items;
-    // 512 threads an SM (by elements 1024): more of them, where they fit, ran the same or slower
-    const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, (V > 2 ? 512 : 1024) / threads));
+    // 512 threads an SM: more of them, where they fit, ran the same or slower
+    const int64_t grid = std::min<int64_t>(ctas, (int64_t)sms * std::max(1, 512 / threads));
     if (grid == ctas) return launch_after(norm_kernel<IO, V, NV, Q, GATE>, grid, threads, 0, stream, p, W);
     // CTAs that walk rows start once the kernel before has left every SM: started as its CTAs leave, more than their
     // share would gather on the SMs that come free first (8191 x 5120 and the product behind it: 172 us against 160)
@@ -337,9 +337,10 @@ cudaError_t launch_nv(const NormParams &p, int W, int sms, cudaStream_t stream) 
 template <typename IO> cudaError_t launch_io(const NormParams &p, int sms, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(IO);
     const int64_t gs = p.D / p.G;
-    // a CTA holds 16 warps at most, a lane up to 3 vectors (6 of longer groups), or 4 pairs (8) or single elements (16)
+    // a CTA holds 16 warps at most, a lane up to 3 vectors (6 of longer groups), or 4 pairs (8), or 8 single elements
+    // (16; with 4 of them 16384 x 1537 took 112 us)
     const int64_t nvec = p.unit == 16 ? gs / V : p.unit == 4 ? gs / 2 : gs;
-    const int few = p.unit == 16 ? 3 : 4, many = p.unit == 16 ? 6 : p.unit == 4 ? 8 : 16;
+    const int few = p.unit == 16 ? 3 : p.unit == 4 ? 4 : 8, many = p.unit == 16 ? 6 : p.unit == 4 ? 8 : 16;
     if (nvec <= kMostWarps * 32 * many && (p.unit == 16 || !p.scales)) {
         const int most = nvec <= kMostWarps * 32 * few ? few : many;
         const int W = (int)((nvec + 32 * most - 1) / (32 * most));
@@ -353,7 +354,7 @@ template <typename IO> cudaError_t launch_io(const NormParams &p, int sms, cudaS
         if constexpr (sizeof(IO) == 2)
             if (p.unit == 4)
                 return NV <= 4 ? launch_nv<IO, 2, 4>(p, W, sms, stream) : launch_nv<IO, 2, 8>(p, W, sms, stream);
-        return NV <= 4 ? launch_nv<IO, 1, 4>(p, W, sms, stream) : launch_nv<IO, 1, 16>(p, W, sms, stream);
+        return NV <= 8 ? launch_nv<IO, 1, 8>(p, W, sms, stream) : launch_nv<IO, 1, 16>(p, W, sms, stream);
     }
     const int64_t grid = std::min<int64_t>(p.rows * p.G, (int64_t)sms * 64);
     norm_long_kernel<IO><<<(unsigned)grid, kThreads, 0, stream>>>(p);
