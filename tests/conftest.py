@@ -28,3 +28,12 @@ def pytest_collection_modifyitems(config, items):
     for it in items:
         if "gpu" in it.keywords:
             it.add_marker(skip)
+
+
+@pytest.fixture(scope="session", autouse=True)
+def native_parts():
+    """Build the library and the binding where either is missing, before the first test."""
+    from mamba_ssd_prefill_gb300 import _build
+
+    if not (os.path.exists(_build.LIB) and os.path.exists(_build.BINDING)):
+        _build.build()
