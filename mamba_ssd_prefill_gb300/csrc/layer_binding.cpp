@@ -110,15 +110,21 @@ void rows(const char *name, const Tensor &t, at::IntArrayRef shape, at::ScalarTy
 void flat(const char *name, const Tensor *t, at::IntArrayRef shape, at::ScalarType type, int dev) {
     if (t && (!is(*t, shape, type, dev) || !t->is_contiguous())) refuse(name, *t, shape, type, dev, "contiguous");
 }
-// [..., K] as evenly spaced rows: their stride
+// [..., K] as evenly spaced rows: their stride. Dimensions of size 1 hold one index, so their strides say nothing.
 int64_t row_stride(const char *name, const Tensor &t, at::IntArrayRef shape, at::ScalarType type, int dev) {
     rows(name, t, shape, type, dev);
     if (shape.size() == 1 || t.is_contiguous()) return shape.back();
     const auto st = t.strides();
-    for (size_t i = 0; i + 2 < shape.size(); ++i)
-        if (shape[i] > 1 && st[i] != st[i + 1] * shape[i + 1])
-            refuse(name, t, shape, type, dev, "evenly spaced rows");
-    return st[shape.size() - 2];
+    int64_t row = shape.back(), next = 0;  // next: what the dimension before must step by
+    bool any = false;
+    for (int64_t i = (int64_t)shape.size() - 2; i >= 0; --i) {
+        if (shape[i] == 1) continue;
+        if (!any) row = st[i];
+        else if (st[i] != next) refuse(name, t, shape, type, dev, "evenly spaced rows");
+        any = true;
+        next = st[i] * shape[i];
+    }
+    return row;
 }
 int device(const char *what, const Tensor &t) {
     if (!t.is_cuda()) throw Refusal{std::string(what) + " runs on CUDA tensors only (there is no CPU path)"};

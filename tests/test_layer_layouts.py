@@ -1,0 +1,78 @@
+"""Layouts of the operators around the SSD: leading dimensions and strides that are read and written where they lie, or
+refused. The elements around a slice hold NaN where it is read and a guard value where it is written."""
+import pytest
+import torch
+
+import mamba_ssd_prefill_gb300 as m
+
+gpu = pytest.mark.gpu
+BF16 = torch.bfloat16
+GUARD = 7.0
+
+
+def cut(base, how):
+    return {"heads": lambda t: t[:, :, 2:4], "half": lambda t: t[:, :, 0], "step": lambda t: t[:, :, ::16],
+            "last": lambda t: t[:, -1:, 8:104], "one": lambda t: t[:, :, 5:6], "row": lambda t: t[:1, -1:, :96]}[how](base)
+
+
+def filled(shape, how, dtype=BF16):
+    """A tensor of `shape` with values in its slice and NaN around it, and the slice."""
+    base = torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+    view = cut(base, how)
+    view.copy_(torch.randn(view.shape, generator=torch.Generator("cpu").manual_seed(len(how))))
+    return base, view
+
+
+# rows at one distance although a dimension of size 1 has another stride: the last token of each prompt, one head of
+# one token a sequence, a step longer than its axis, one row
+EVEN = [((5, 7, 200), "last"), ((4, 1, 8, 64), "one"), ((4, 1, 8, 64), "step"), ((3, 4, 150), "row")]
+# rows at two distances: some heads of one token a sequence, one half of two; of several tokens
+UNEVEN = [((4, 1, 8, 64), "heads"), ((4, 1, 2, 8, 64), "half"), ((2, 3, 8, 64), "heads")]
+
+
+@gpu
+@pytest.mark.parametrize("shape,how", EVEN, ids=[h for _, h in EVEN])
+def test_rows_of_one_distance_are_read_and_written_where_they_lie(shape, how):
+    _, x = filled(shape, how)
+    _, z = filled(shape, how)
+    xc, zc = x.contiguous(), z.contiguous()
+    want = m.ssd_group_norm(xc, z=zc)
+    assert bool(torch.isfinite(want).all())
+    assert torch.equal(m.ssd_group_norm(x, z=z), want)
+    to = torch.full(shape, GUARD, dtype=BF16, device="cuda")
+    y = m.ssd_group_norm(x, z=z, y=cut(to, how))
+    assert torch.equal(y, want)
+    y.fill_(GUARD)
+    assert bool((to == GUARD).all())
+    q, s = m.ssd_fp8_quantize(x)
+    qc, sc = m.ssd_fp8_quantize(xc)
+    assert torch.equal(q.view(torch.uint8), qc.view(torch.uint8)) and torch.equal(s, sc)
+    w, ws = m.ssd_fp8_quantize(torch.randn(x.shape[-1], x.shape[-1], generator=torch.Generator("cpu").manual_seed(1)).cuda(), 128)
+    want = m.ssd_fp8_matmul(qc, sc, w, ws)
+    out = m.ssd_fp8_matmul(qc, sc, w, ws, out=cut(to, how))
+    assert torch.equal(out, want)
+    out.fill_(GUARD)
+    assert bool((to == GUARD).all())
+
+
+@gpu
+@pytest.mark.parametrize("shape,how", UNEVEN, ids=[f"{h}{len(s)}-{s[1]}" for s, h in UNEVEN])
+def test_rows_of_two_distances_are_refused(shape, how):
+    _, x = filled(shape, how)
+    xc = x.contiguous()
+    to = torch.full(shape, GUARD, dtype=BF16, device="cuda")
+    q, s = m.ssd_fp8_quantize(xc)
+    w, ws = m.ssd_fp8_quantize(torch.ones(64, 64, device="cuda"), 128)
+    for call in (lambda: m.ssd_group_norm(x), lambda: m.ssd_group_norm(xc, z=x),
+                 lambda: m.ssd_group_norm(xc, y=cut(to, how)), lambda: m.ssd_fp8_quantize(x),
+                 lambda: m.ssd_fp8_matmul(q, s, w, ws, out=cut(to, how))):
+        with pytest.raises(ValueError, match="evenly spaced"):
+            call()
+    assert bool((to == GUARD).all())
+
+
+@gpu
+def test_rows_at_distance_zero():
+    x = torch.randn(1, 1, 1, 64, generator=torch.Generator("cpu").manual_seed(3)).to(BF16).cuda()
+    for shape in ((2, 6, 1, 64), (2, 1, 6, 64)):
+        assert torch.equal(m.ssd_group_norm(x.expand(shape)), m.ssd_group_norm(x).expand(shape))
