@@ -8,6 +8,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/from_blob.h>
+#include <ATen/ops/maximum.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -18,8 +20,10 @@
 #include <map>
 #include <optional>
 #include <sstream>
+#include <stdexcept>
 #include <string>
-#include <tuple>
+#include <utility>
+#include <vector>
 
 #include "../../include/ssd.h"
 
@@ -132,6 +136,45 @@ int device(const char *what, const Tensor &t) {
 }
 void *ptr(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
 
+void cuda_ok(cudaError_t e, const char *what) {
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        throw std::runtime_error(std::string(what) + ": " + cudaGetErrorString(e));
+    }
+}
+
+// The status header (256 bytes) of all calls on a device that are given no workspace: kernels only ever set its status,
+// so any calls may share it. It is no memory of PyTorch's, so that a call inside a capture finds it zeroed and at an
+// address that stays, whatever becomes of the graph. Called with the device current.
+const Tensor &device_status(int dev) {
+    static auto *all = new std::map<int, Tensor>();
+    Tensor &t = (*all)[dev];
+    if (!t.defined()) {
+        constexpr int64_t kBytes = 256;
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // an allocation beside a capture
+        cuda_ok(cudaThreadExchangeStreamCaptureMode(&mode), "the status header");
+        void *p = nullptr;
+        cudaStream_t s = nullptr;
+        cudaError_t e = cudaMalloc(&p, kBytes);
+        if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+        if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, kBytes, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (s) (void)cudaStreamDestroy(s);
+        if (e != cudaSuccess && p) (void)cudaFree(p);
+        (void)cudaThreadExchangeStreamCaptureMode(&mode);
+        cuda_ok(e, "the status header");
+        t = at::from_blob(p, {kBytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+    }
+    return t;
+}
+Tensor status_word(const Tensor &header) { return header.narrow(0, 12, 4).view(at::kInt); }
+
+// Workspaces of calls that need more than the header: one per device and stream, grown, kept for the process's life.
+std::map<std::pair<int, cudaStream_t>, Tensor> &stream_workspaces() {
+    static auto *kept = new std::map<std::pair<int, cudaStream_t>, Tensor>();
+    return *kept;
+}
+
 // Device, stream and workspace of one call.
 struct Call {
     int dev;
@@ -139,8 +182,9 @@ struct Call {
     std::optional<c10::cuda::CUDAStreamGuard> on;  // another stream than the current one: outputs belong to it
     c10::cuda::CUDAStream stream;
     Tensor ws;
+    bool of_capture = false;  // ws is scratch of the graph that is being captured
 
-    Call(int dev_, PyObject *stream_, PyObject *workspace, int use, size_t bytes)
+    Call(int dev_, PyObject *stream_, PyObject *workspace, size_t bytes)
         : dev(dev_), guard((c10::DeviceIndex)dev_), stream(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev_)) {
         if (stream_ != Py_None) {
             auto get = [&](const char *name) {
@@ -159,17 +203,13 @@ struct Call {
                 stream = s;
             }
         }
-        if (workspace == Py_None) {  // one per use, device and stream, kept for the process's life
-            static auto *kept = new std::map<std::tuple<int, int, cudaStream_t>, Tensor>();
-            Tensor &t = (*kept)[{use, dev, stream.stream()}];
-            if (!t.defined() || (size_t)t.numel() < bytes)
-                t = at::zeros({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
-            ws = t;
+        if (workspace == Py_None) {
+            own(bytes);
             return;
         }
-        const int own = PyObject_IsInstance(workspace, workspace_class);
-        if (own < 0) throw Raised{};
-        if (own) {
+        const int is_workspace = PyObject_IsInstance(workspace, workspace_class);
+        if (is_workspace < 0) throw Raised{};
+        if (is_workspace) {
             PyObject *t = PyObject_CallMethod(workspace, "get", "n", (Py_ssize_t)bytes);
             if (!t) throw Raised{};
             if (THPVariable_Check(t)) ws = THPVariable_Unpack(t);
@@ -179,6 +219,41 @@ struct Call {
         }
         if (!ws.defined() || !ws.is_cuda() || ws.get_device() != dev || !ws.is_contiguous())
             throw Refusal{"workspace: expected a Workspace, or a contiguous tensor on the tensors' device"};
+    }
+    // The workspace of a call that is given none. A graph that is being captured gets scratch of its own, from its own
+    // memory: the stream's workspace may be replaced by a larger one while the graph lives, and graphs captured on one
+    // stream may be replayed on several. A captured call of the scan so takes two small nodes more (the header zeroed,
+    // its status passed on); those that need only the header take none.
+    void own(size_t bytes) {
+        const Tensor &status = device_status(dev);
+        if (bytes <= (size_t)status.numel()) {
+            ws = status;
+            return;
+        }
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        cuda_ok(cudaStreamIsCapturing(stream.stream(), &capture), "the workspace");
+        if (capture != cudaStreamCaptureStatusNone) {
+            of_capture = true;
+            ws = make({(int64_t)bytes}, at::kByte);
+            ws.narrow(0, 0, status.numel()).zero_();
+            return;
+        }
+        Tensor &t = stream_workspaces()[{dev, stream.stream()}];
+        if (!t.defined() || (size_t)t.nbytes() < bytes) {
+            Tensor larger = at::zeros({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+            if (t.defined()) {  // what the smaller one has reported and nobody has read
+                Tensor word = status_word(larger);
+                word.copy_(status_word(t));
+            }
+            t = larger;
+        }
+        ws = t;
+    }
+    // After the launch: the status of a graph's own scratch goes to the header that outlives it.
+    void pass_status_on() const {
+        if (!of_capture) return;
+        Tensor to = status_word(device_status(dev));
+        at::maximum_out(to, to, status_word(ws));
     }
     size_t ws_bytes() const { return (size_t)ws.nbytes(); }
     Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
@@ -191,7 +266,6 @@ struct Call {
                 if (t && t->defined()) t->record_stream(stream);
     }
 };
-enum Use { kScan, kConv, kNorm, kFp8 };
 
 void check(int status, const char *what) {
     if (status) throw Status{status, what};
@@ -267,7 +341,7 @@ PyObject *selective_scan(PyObject *const *a) {
     c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
     size_t bytes = 0;
     check(f_scan_size(&p, &bytes), what);
-    Call call(dev, a[16], a[15], kScan, bytes);
+    Call call(dev, a[16], a[15], bytes);
     const Tensor y = yt ? *yt : call.make(shape, io);
     const bool with_final = ft || truth(a[14]);
     const Tensor fin = ft ? *ft : with_final ? call.make(sshape, state) : Tensor();
@@ -291,6 +365,7 @@ PyObject *selective_scan(PyObject *const *a) {
     t.c_seq = C.stride(0), t.c_tok = C.stride(1);
     t.y_seq = y.stride(0), t.y_tok = y.stride(1);
     check(f_scan(&p, &t, call.ws.data_ptr(), call.ws_bytes(), call.stream.stream()), what);
+    call.pass_status_on();
     call.keep({&x, &dt, bias, &A, &B, &C, D, z, init, cu, &y, &fin, &call.ws});
     return pair(y, fin, with_final);
 }
@@ -324,7 +399,7 @@ PyObject *conv(PyObject *const *a) {
     flat("conv_state", state, sshape, io, dev);
     flat("conv_state_out", st, sshape, io, dev);
     if (ot) rows("out", *ot, shape, io, dev);
-    Call call(dev, a[10], a[9], kConv, 256);
+    Call call(dev, a[10], a[9], 256);
     const Tensor out = ot ? *ot : call.make(shape, io);
     const bool with_state = st || truth(a[8]);
     const Tensor left = st ? *st : with_state ? call.make(sshape, io) : Tensor();
@@ -380,7 +455,7 @@ PyObject *group_norm(PyObject *const *a) {
     t.y_row = yt ? row_stride("y", *yt, shape, out, dev) : Dc;
     flat("weight", w, {Dc}, at::kFloat, dev);
     flat("bias", bias, {Dc}, at::kFloat, dev);
-    Call call(dev, a[12], a[11], kNorm, 256);
+    Call call(dev, a[12], a[11], 256);
     const Tensor y = yt ? *yt : call.make(shape, out);
     const Tensor scales = quantize ? call.make(with_last(shape, (Dc + 127) / 128), at::kFloat) : Tensor();
     t.x = x.data_ptr();
@@ -409,7 +484,7 @@ PyObject *fp8_quantize(PyObject *const *a) {
     const auto shape = x.sizes();
     const int64_t K = shape.back(), n = K ? x.numel() / K : 0, kb = (K + 127) / 128;
     const int64_t row = row_stride("x", x, shape, io, dev);
-    Call call(dev, a[3], a[2], kFp8, 256);
+    Call call(dev, a[3], a[2], 256);
     const Tensor q = call.make(shape, at::kFloat8_e4m3fn);
     const Tensor scales = block_rows == 1 ? call.make(with_last(shape, kb), at::kFloat)
                                           : call.make({(n + 127) / 128, kb}, at::kFloat);
@@ -447,7 +522,7 @@ PyObject *fp8_matmul(PyObject *const *v) {
     for (int64_t i = 0; i + 1 < a.dim(); ++i) M *= a.size(i);
     const auto shape = with_last(a.sizes(), N);
     const int64_t row = ot ? row_stride("out", *ot, shape, type, dev) : N;
-    Call call(dev, v[8], v[7], kFp8, 256);
+    Call call(dev, v[8], v[7], 256);
     const Tensor out = ot ? *ot : call.make(shape, type);
     ssd_matmul_problem_t p{M, N, K, code, 0};
     check(f_matmul(&p, a.data_ptr(), static_cast<const float *>(sa.data_ptr()), b.data_ptr(),
