@@ -143,7 +143,11 @@ def kernel_for(prob: SsdProblem) -> str:
 
 
 class Workspace:
-    """A zero-initialised device workspace, grown on demand and reused across calls on one stream."""
+    """A zero-initialised device workspace, grown on demand and reused across calls on one stream.
+
+    A buffer that a captured graph uses lives as long as the Workspace, also when a later call needs a larger one, and
+    one that is first needed inside a capture is zeroed at once, outside of the graph. Graphs captured with one
+    Workspace must not be replayed at the same time."""
 
     # the state-passing tags carry the launch count modulo 2^22: the buffer is zero-filled again well before that
     REZERO_EVERY = 1 << 21
@@ -152,16 +156,37 @@ class Workspace:
         self.device = torch.device(device or "cuda")
         self.buf = None
         self.calls = 0
+        self.in_graphs = False  # a captured graph uses buf
+        self.held = []          # smaller buffers that captured graphs use
 
     def get(self, nbytes: int) -> torch.Tensor:
+        capturing = torch.cuda.is_current_stream_capturing()
         if self.buf is None or self.buf.numel() < nbytes:
             # the library asks for a zero-filled workspace on first use only
-            self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            nbytes = max(nbytes, 256)
+            if capturing:
+                from . import layer
+
+                index = torch.cuda.current_device() if self.device.index is None else self.device.index
+                new = layer._bind().zeros_outside(nbytes, index)
+            else:
+                new = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            if self.buf is not None:
+                if capturing or self.in_graphs:
+                    self.held.append(self.buf)
+                else:
+                    new[12:16] = self.buf[12:16]  # the header's status: what has been reported and not been read
+            self.buf, self.in_graphs = new, False
             self.calls = 0
+        self.in_graphs |= capturing
         self.calls += 1
         if self.calls % self.REZERO_EVERY == 0:
             self.buf.zero_()  # on the current stream, ordered before the call that uses it
         return self.buf
+
+    def buffers(self) -> list:
+        """Every buffer that calls may have reported to."""
+        return [*self.held, self.buf] if self.buf is not None else []
 
 
 _default_ws: dict = {}
@@ -393,12 +418,10 @@ def ssd_fwd_conv(xbc, conv_weight, dt_raw, dt_bias, A, nheads, headdim, ngroups,
 
 def check(workspace, stream=None):
     """Synchronise and raise SsdError if a device-side wait failed in an earlier call."""
-    ws = workspace.buf if isinstance(workspace, Workspace) else workspace
-    if ws is None:
-        return
-    st = lib().ssd_fwd_check(_ptr(ws), _stream_ptr(stream, ws.device))
-    if st:
-        raise SsdError(st, "ssd_fwd_check")
+    for ws in workspace.buffers() if isinstance(workspace, Workspace) else [workspace] if workspace is not None else []:
+        st = lib().ssd_fwd_check(_ptr(ws), _stream_ptr(stream, ws.device))
+        if st:
+            raise SsdError(st, "ssd_fwd_check")
 
 
 def debug_set(workspace, timeout_ns=0, skip_publish=-1, stream=None):

@@ -143,28 +143,38 @@ void cuda_ok(cudaError_t e, const char *what) {
     }
 }
 
+// Zeroed memory that is none of PyTorch's, also while a graph is being captured: it lies outside of the graph's memory and
+// is zeroed now, not at each replay. Freed with the tensor. Called with the device current.
+Tensor zeros_outside(int64_t bytes, int dev) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // an allocation beside a capture
+    cuda_ok(cudaThreadExchangeStreamCaptureMode(&mode), "a workspace");
+    void *p = nullptr;
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaMalloc(&p, (size_t)bytes);
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)bytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (s) (void)cudaStreamDestroy(s);
+    if (e != cudaSuccess && p) (void)cudaFree(p);
+    (void)cudaThreadExchangeStreamCaptureMode(&mode);
+    cuda_ok(e, "a workspace");
+    auto release = [](void *q) {
+        cudaStreamCaptureMode m = cudaStreamCaptureModeRelaxed;
+        const bool changed = cudaThreadExchangeStreamCaptureMode(&m) == cudaSuccess;
+        (void)cudaFree(q);
+        if (changed) (void)cudaThreadExchangeStreamCaptureMode(&m);
+    };
+    return at::from_blob(p, {bytes}, release,
+                         at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+}
+
 // The status header (256 bytes) of all calls on a device that are given no workspace: kernels only ever set its status,
-// so any calls may share it. It is no memory of PyTorch's, so that a call inside a capture finds it zeroed and at an
-// address that stays, whatever becomes of the graph. Called with the device current.
+// so any calls may share it, and a call inside a capture finds it zeroed and at an address that stays, whatever becomes
+// of the graph. Called with the device current.
 const Tensor &device_status(int dev) {
     static auto *all = new std::map<int, Tensor>();
     Tensor &t = (*all)[dev];
-    if (!t.defined()) {
-        constexpr int64_t kBytes = 256;
-        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // an allocation beside a capture
-        cuda_ok(cudaThreadExchangeStreamCaptureMode(&mode), "the status header");
-        void *p = nullptr;
-        cudaStream_t s = nullptr;
-        cudaError_t e = cudaMalloc(&p, kBytes);
-        if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
-        if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, kBytes, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-        if (s) (void)cudaStreamDestroy(s);
-        if (e != cudaSuccess && p) (void)cudaFree(p);
-        (void)cudaThreadExchangeStreamCaptureMode(&mode);
-        cuda_ok(e, "the status header");
-        t = at::from_blob(p, {kBytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
-    }
+    if (!t.defined()) t = zeros_outside(256, dev);
     return t;
 }
 Tensor status_word(const Tensor &header) { return header.narrow(0, 12, 4).view(at::kInt); }
@@ -561,6 +571,23 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// zeros_outside(bytes, device index), for the Workspace class
+PyObject *zeros(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 2) {
+        PyErr_Format(PyExc_TypeError, "expected 2 arguments, got %zd", n);
+        return nullptr;
+    }
+    try {
+        const int64_t bytes = whole(args[0]), dev = whole(args[1]);
+        c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        return THPVariable_Wrap(zeros_outside(bytes, (int)dev));
+    } catch (const Raised &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses of the six C entries in the order above, SsdError, Workspace)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 8) {
@@ -593,6 +620,7 @@ template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)> PyMethodDef
 }
 PyMethodDef methods[] = {
     method<bind>("bind"),
+    method<zeros>("zeros_outside"),
     method<entry<selective_scan, 17>>("selective_scan"),
     method<entry<conv, 11>>("conv"),
     method<entry<group_norm, 13>>("group_norm"),

@@ -88,3 +88,90 @@ def test_a_stream_s_workspace_grows_between_calls():
         got = scan(t, stream=side)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def call_of(kind, ws, L=700, larger=False):
+    """A call of the SSD or of the selective scan; `larger`: one that needs more workspace."""
+    if kind == "ssd":
+        from mamba_ssd_prefill_gb300.inputs import WORKLOADS, make_inputs
+
+        inp = make_inputs(WORKLOADS["m130-bf16"].with_(batch=6 if larger else 1, seqlen=L, nheads=4, seed=11),
+                          device="cuda")
+        return lambda: m.ssd_fwd(**inp, workspace=ws)
+    t = scan_inputs(1, 20000 if larger else L, 64, 16, seed=11)
+    return lambda: scan(t, workspace=ws)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["ssd", "scan"])
+def test_a_workspace_keeps_what_a_graph_uses(kind):
+    """A Workspace that grows after a capture: the graph's buffer stays its own."""
+    ws = m.Workspace("cuda")
+    small, large = call_of(kind, ws), call_of(kind, ws, larger=True)
+    want = [o.clone() for o in call_of(kind, m.Workspace("cuda"))()]
+    small()
+    before = ws.buf.numel()
+    side = torch.cuda.Stream()
+    graph, out = captured(small, side)
+    at = ws.buf.data_ptr()
+    with torch.cuda.stream(side):
+        large()
+        assert ws.buf.numel() > before and at in [b.data_ptr() for b in ws.held]
+        fillers = [torch.full((before // 4,), 3.0, device="cuda") for _ in range(8)]
+        for _ in range(2):
+            graph.replay()
+            assert all(torch.equal(o, w) for o, w in zip(out, want))
+        assert all(bool((f == 3).all()) for f in fillers)
+    m.check(ws, side)
+    plain = m.Workspace("cuda")  # without a graph nothing is held
+    for larger in (False, True):
+        call_of(kind, plain, larger=larger)()
+    assert not plain.held
+    m.check(plain)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["ssd", "scan"])
+def test_a_workspace_first_used_inside_a_capture(kind):
+    ws = m.Workspace("cuda")
+    call = call_of(kind, ws, 900)
+    want = [o.clone() for o in call_of(kind, m.Workspace("cuda"), 900)()]
+    side = torch.cuda.Stream()
+    graph, out = captured(call, side)
+    with torch.cuda.stream(side):
+        m.check(ws, side)  # nothing has run, nothing is reported
+        assert all(torch.equal(o, w) for o, w in zip(call(), want))
+        for _ in range(3):
+            graph.replay()
+            assert all(torch.equal(o, w) for o, w in zip(out, want))
+    m.check(ws, side)
+
+
+@gpu
+def test_a_process_whose_first_call_is_captured():
+    """The header of calls without a workspace does not exist before the capture."""
+    import os
+    import subprocess
+    import sys
+
+    code = """if True:
+        import torch, mamba_ssd_prefill_gb300 as m
+        x = torch.randn(4, 256, device="cuda").bfloat16()
+        t = dict(x=torch.ones(1, 900, 64, device="cuda"), dt_raw=torch.zeros(1, 900, 64, device="cuda"), dt_bias=None,
+                 A=-torch.ones(64, 16, device="cuda"), B=torch.ones(1, 900, 1, 16, device="cuda"),
+                 C=torch.ones(1, 900, 1, 16, device="cuda"))
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            n = m.ssd_group_norm(x)
+            y, f = m.ssd_selective_scan(**t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(n, m.ssd_group_norm(x))
+        y2, f2 = m.ssd_selective_scan(**t)
+        assert torch.equal(y, y2) and torch.equal(f, f2)
+        print("same")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
