@@ -416,9 +416,24 @@ def ssd_fwd_conv(xbc, conv_weight, dt_raw, dt_bias, A, nheads, headdim, ngroups,
     return y, final_states, conv_state_out, xbc_out
 
 
-def check(workspace, stream=None):
-    """Synchronise and raise SsdError if a device-side wait failed in an earlier call."""
-    for ws in workspace.buffers() if isinstance(workspace, Workspace) else [workspace] if workspace is not None else []:
+def check(workspace=None, stream=None):
+    """Synchronise `stream` (default: the current one) and raise SsdError if an earlier call reported a device-side
+    error: a wait that gave up, malformed offsets. `workspace` is the Workspace or tensor that the calls were given;
+    without it, the calls that were given none are checked (those of `stream`; of the operators in layer.py, where they
+    need no more than a status header, those of its device)."""
+    if isinstance(workspace, Workspace):
+        buffers = workspace.buffers()
+    elif workspace is not None:
+        buffers = [workspace]
+    else:
+        from . import layer
+
+        s = stream if stream is not None else torch.cuda.current_stream()
+        key = (s.device.index, s.cuda_stream)
+        buffers = [b for k in (key, ("host", *key)) if k in _default_ws for b in _default_ws[k].buffers()]
+        buffers += layer._bind().reported(*key)
+        stream = s
+    for ws in buffers:
         st = lib().ssd_fwd_check(_ptr(ws), _stream_ptr(stream, ws.device))
         if st:
             raise SsdError(st, "ssd_fwd_check")

@@ -168,12 +168,15 @@ Tensor zeros_outside(int64_t bytes, int dev) {
                          at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
 }
 
+std::map<int, Tensor> &device_headers() {
+    static auto *all = new std::map<int, Tensor>();
+    return *all;
+}
 // The status header (256 bytes) of all calls on a device that are given no workspace: kernels only ever set its status,
 // so any calls may share it, and a call inside a capture finds it zeroed and at an address that stays, whatever becomes
 // of the graph. Called with the device current.
 const Tensor &device_status(int dev) {
-    static auto *all = new std::map<int, Tensor>();
-    Tensor &t = (*all)[dev];
+    Tensor &t = device_headers()[dev];
     if (!t.defined()) t = zeros_outside(256, dev);
     return t;
 }
@@ -615,12 +618,39 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// reported(device index, stream): the buffers whose headers hold the status of calls without a workspace on that stream
+PyObject *reported(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 2) {
+        PyErr_Format(PyExc_TypeError, "expected 2 arguments, got %zd", n);
+        return nullptr;
+    }
+    try {
+        const int dev = (int)whole(args[0]);
+        void *stream = PyLong_AsVoidPtr(args[1]);
+        if (PyErr_Occurred()) return nullptr;
+        std::vector<Tensor> found;
+        const auto h = device_headers().find(dev);
+        if (h != device_headers().end() && h->second.defined()) found.push_back(h->second);
+        const auto w = stream_workspaces().find({dev, static_cast<cudaStream_t>(stream)});
+        if (w != stream_workspaces().end() && w->second.defined()) found.push_back(w->second);
+        PyObject *list = PyList_New((Py_ssize_t)found.size());
+        if (!list) return nullptr;
+        for (size_t i = 0; i < found.size(); ++i) PyList_SET_ITEM(list, (Py_ssize_t)i, THPVariable_Wrap(found[i]));
+        return list;
+    } catch (const Raised &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)> PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {
     method<bind>("bind"),
     method<zeros>("zeros_outside"),
+    method<reported>("reported"),
     method<entry<selective_scan, 17>>("selective_scan"),
     method<entry<conv, 11>>("conv"),
     method<entry<group_norm, 13>>("group_norm"),

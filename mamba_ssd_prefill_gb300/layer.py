@@ -7,9 +7,10 @@ built in-tree as ``_layer.so``): for a single token it would take longer than th
 slices of wider rows (the last dimension contiguous, any other stride). `stream` (default: the current one) is the
 stream the kernels run on; with another than the current stream the outputs are allocated for it, and the inputs are
 kept until its work is done. `workspace` (a Workspace) carries the device status that check() reads. Without it a call
-takes a status header of its device and, for a scan in segments, a buffer of its device and stream that grows; a graph
-that is being captured takes such a buffer from its own memory, so that it may be replayed on any stream whatever is
-called in between. Graphs captured with one and the same Workspace must not be replayed at the same time.
+takes a status header of its device (check() without a workspace reads it) and, for a scan in segments, a buffer of its
+device and stream that grows; a graph that is being captured takes such a buffer from its own memory, so that it may be
+replayed on any stream whatever is called in between. Graphs captured with one and the same Workspace must not be
+replayed at the same time.
 """
 from __future__ import annotations
 
@@ -54,7 +55,7 @@ def ssd_selective_scan(x, dt_raw, dt_bias, A, B, C, D=None, z=None, init_states=
     dt = softplus(dt_raw + dt_bias): h = exp(dt A) h + dt x B, y = (h . C + D x) z sigmoid(z), in fp32. cu_seqlens
     (int32 [nseq + 1], on the GPU) packs nseq sequences on the token axis of [1, T, ...] tensors; the states are then
     [nseq, Dc, N]. final_states may be init_states itself (a cache advanced in place). Returns (y, final_states or
-    None). Malformed offsets are reported by check() on the workspace."""
+    None). Malformed offsets are reported by check()."""
     return (_native or _bind()).selective_scan(x, dt_raw, dt_bias, A, B, C, D, z, init_states, cu_seqlens, state_dtype,
                                                softplus, y, final_states, return_final_states, workspace, stream)
 

@@ -175,3 +175,50 @@ def test_a_process_whose_first_call_is_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+BAD = [0, 300, 200, 900]  # offsets that decrease
+
+
+@gpu
+def test_errors_of_calls_without_a_workspace_are_reported():
+    """Malformed offsets, in a scan with a workspace of its stream, in one that needs only the header, in the
+    convolution, in a stream's workspace that grew since, and in replays of a graph."""
+    bad = torch.tensor(BAD, dtype=torch.int32, device="cuda")
+    good = torch.tensor([0, 200, 300, 900], dtype=torch.int32, device="cuda")
+    t = scan_inputs(1, 900, 64, 16, lengths=[200, 100, 600], seed=3)
+    tiny = scan_inputs(1, 9, 64, 16, lengths=[2, 3, 4], seed=3)
+    tiny_bad = {**tiny, "cu_seqlens": torch.tensor([0, 3, 2, 9], dtype=torch.int32, device="cuda")}
+    w = torch.ones(64, 4, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def reports():
+        with pytest.raises(m.SsdError) as e:
+            m.check()
+        assert e.value.status == 1
+        m.check()  # read once
+
+    with torch.cuda.stream(side):
+        m.check()
+        scan({**t, "cu_seqlens": bad})
+        reports()
+        scan(tiny_bad)
+        reports()
+        m.ssd_conv(t["x"], w, cu_seqlens=bad)
+        reports()
+        scan({**t, "cu_seqlens": bad})
+        scan(scan_inputs(1, 30000, 64, 16, seed=5))  # the workspace grows
+        reports()
+    offsets = good.clone()
+    graph, _ = captured(lambda: scan({**t, "cu_seqlens": offsets}), side)
+    with torch.cuda.stream(side):
+        graph.replay()
+        m.check()
+        offsets.copy_(bad)
+        graph.replay()
+        offsets.copy_(good)
+        graph.replay()
+        reports()
+    m.check(stream=side)
+    m.check()
