@@ -147,7 +147,7 @@ class Workspace:
 
     A buffer that a captured graph uses lives as long as the Workspace, also when a later call needs a larger one, and
     one that is first needed inside a capture is zeroed at once, outside of the graph. Graphs captured with one
-    Workspace must not be replayed at the same time."""
+    Workspace must not be replayed at the same time. Calls of the SSD and of the operators around it may share one."""
 
     # the state-passing tags carry the launch count modulo 2^22: the buffer is zero-filled again well before that
     REZERO_EVERY = 1 << 21
@@ -158,6 +158,7 @@ class Workspace:
         self.calls = 0
         self.in_graphs = False  # a captured graph uses buf
         self.held = []          # smaller buffers that captured graphs use
+        self.layer = None       # the Workspace of the operators around the SSD
 
     def get(self, nbytes: int) -> torch.Tensor:
         capturing = torch.cuda.is_current_stream_capturing()
@@ -184,9 +185,17 @@ class Workspace:
             self.buf.zero_()  # on the current stream, ordered before the call that uses it
         return self.buf
 
+    def get_layer(self, nbytes: int) -> torch.Tensor:
+        """The same for the operators around the SSD, in a buffer apart: the scan keeps its segments' states where
+        ssd_fwd expects the tags that its calls left."""
+        if self.layer is None:
+            self.layer = Workspace(self.device)
+        return self.layer.get(nbytes)
+
     def buffers(self) -> list:
         """Every buffer that calls may have reported to."""
-        return [*self.held, self.buf] if self.buf is not None else []
+        own = [*self.held, self.buf] if self.buf is not None else []
+        return own + self.layer.buffers() if self.layer is not None else own
 
 
 _default_ws: dict = {}

@@ -223,7 +223,7 @@ struct Call {
         const int is_workspace = PyObject_IsInstance(workspace, workspace_class);
         if (is_workspace < 0) throw Raised{};
         if (is_workspace) {
-            PyObject *t = PyObject_CallMethod(workspace, "get", "n", (Py_ssize_t)bytes);
+            PyObject *t = PyObject_CallMethod(workspace, "get_layer", "n", (Py_ssize_t)bytes);
             if (!t) throw Raised{};
             if (THPVariable_Check(t)) ws = THPVariable_Unpack(t);
             Py_DECREF(t);

@@ -6,7 +6,8 @@ pointers; the computation runs in the library's kernels. The marshalling itself 
 built in-tree as ``_layer.so``): for a single token it would take longer than the kernel. Token tensors may be column
 slices of wider rows (the last dimension contiguous, any other stride). `stream` (default: the current one) is the
 stream the kernels run on; with another than the current stream the outputs are allocated for it, and the inputs are
-kept until its work is done. `workspace` (a Workspace) carries the device status that check() reads. Without it a call
+kept until its work is done. `workspace` (a Workspace) carries the device status that check() reads; it may serve ssd_fwd's
+calls too, a plain tensor in its place must not. Without it a call
 takes a status header of its device (check() without a workspace reads it) and, for a scan in segments, a buffer of its
 device and stream that grows; a graph that is being captured takes such a buffer from its own memory, so that it may be
 replayed on any stream whatever is called in between. Graphs captured with one and the same Workspace must not be

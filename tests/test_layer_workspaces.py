@@ -110,13 +110,13 @@ def test_a_workspace_keeps_what_a_graph_uses(kind):
     small, large = call_of(kind, ws), call_of(kind, ws, larger=True)
     want = [o.clone() for o in call_of(kind, m.Workspace("cuda"))()]
     small()
-    before = ws.buf.numel()
+    before = ws.buffers()[-1].numel()
     side = torch.cuda.Stream()
     graph, out = captured(small, side)
-    at = ws.buf.data_ptr()
+    at = ws.buffers()[-1].data_ptr()
     with torch.cuda.stream(side):
         large()
-        assert ws.buf.numel() > before and at in [b.data_ptr() for b in ws.held]
+        assert ws.buffers()[-1].numel() > before and at in [b.data_ptr() for b in ws.buffers()[:-1]]
         fillers = [torch.full((before // 4,), 3.0, device="cuda") for _ in range(8)]
         for _ in range(2):
             graph.replay()
@@ -126,7 +126,7 @@ def test_a_workspace_keeps_what_a_graph_uses(kind):
     plain = m.Workspace("cuda")  # without a graph nothing is held
     for larger in (False, True):
         call_of(kind, plain, larger=larger)()
-    assert not plain.held
+    assert len(plain.buffers()) == 1
     m.check(plain)
 
 
@@ -222,3 +222,23 @@ def test_errors_of_calls_without_a_workspace_are_reported():
         reports()
     m.check(stream=side)
     m.check()
+
+
+@gpu
+def test_one_workspace_for_the_ssd_and_the_operators_around_it():
+    """The scan's states do not land on the tags that ssd_fwd's calls leave behind, nor the other way round."""
+    ws = m.Workspace("cuda")
+    calls = [call_of(k, ws, L) for k, L in (("ssd", 700), ("scan", 3000), ("ssd", 300), ("scan", 900))]
+    wants = [[o.clone() for o in call_of(k, m.Workspace("cuda"), L)()]
+             for k, L in (("ssd", 700), ("scan", 3000), ("ssd", 300), ("scan", 900))]
+    for _ in range(3):
+        for call, want in zip(calls, wants):
+            assert all(torch.equal(o, w) for o, w in zip(call(), want))
+            m.check(ws)
+    t = scan_inputs(1, 900, 64, 16, lengths=[200, 100, 600], seed=3)
+    scan({**t, "cu_seqlens": torch.tensor(BAD, dtype=torch.int32, device="cuda")}, workspace=ws)
+    calls[0]()
+    with pytest.raises(m.SsdError) as e:
+        m.check(ws)
+    assert e.value.status == 1
+    m.check(ws)
