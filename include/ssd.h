@@ -345,7 +345,8 @@ typedef struct {
     int32_t io_dtype;   /* ssd_dtype_t of x, dt_raw, B, C, z, y                  */
     int32_t state_dtype;/* SSD_F32 or SSD_F16                                    */
     int32_t packed;     /* 1: the sequences lie one after the other on one axis of
-                           seqlen tokens, sequence s on [cu_seqlens[s], cu_seqlens[s+1]) */
+                           seqlen tokens, sequence s on [cu_seqlens[s], cu_seqlens[s+1]);
+                           tokens need a sequence: batch >= 1 where seqlen > 0   */
     int32_t softplus;   /* 0 or 1                                                */
 } ssd_scan_problem_t;
 

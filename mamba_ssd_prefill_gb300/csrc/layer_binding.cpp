@@ -308,6 +308,7 @@ int sequences(const char *what, const Tensor &x, const Tensor *cu, int64_t &nseq
             cu->numel() < 1 || !cu->is_contiguous())
             throw Refusal{"cu_seqlens: expected a contiguous int32 [nseq + 1] tensor on the device of x"};
         nseq = cu->numel() - 1;
+        if (nseq == 0 && x.size(1) > 0) throw Refusal{"cu_seqlens: offsets of no sequences, but x has tokens"};
     }
     return dev;
 }

@@ -40,6 +40,7 @@ ssd_status_t check_scan(const ssd_scan_problem_t *p) {
         !fits((double)p->batch, (double)p->channels, (double)p->dstate))
         return SSD_ERR_INVALID_ARG;
     if (p->packed && (p->batch > INT32_MAX - 1 || p->seqlen > INT32_MAX)) return SSD_ERR_INVALID_ARG;
+    if (p->packed && p->batch == 0 && p->seqlen > 0) return SSD_ERR_INVALID_ARG;  // tokens of no sequence
     if (p->dstate > 256) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -230,6 +231,7 @@ SSD_API ssd_status_t ssd_conv(const ssd_conv_problem_t *prob, const ssd_conv_ten
     if ((pr.packed != 0 && pr.packed != 1) || (pr.activation != SSD_ACT_NONE && pr.activation != SSD_ACT_SILU))
         return SSD_ERR_INVALID_ARG;
     if (pr.packed && (pr.batch > INT32_MAX - 1 || pr.seqlen > INT32_MAX)) return SSD_ERR_INVALID_ARG;
+    if (pr.packed && pr.batch == 0 && pr.seqlen > 0) return SSD_ERR_INVALID_ARG;  // tokens of no sequence
     if (!fits((double)pr.batch * (double)pr.seqlen, (double)pr.channels) ||
         !fits((double)pr.batch, (double)pr.channels, 8.0))
         return SSD_ERR_INVALID_ARG;

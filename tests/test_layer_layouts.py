@@ -1,5 +1,8 @@
 """Layouts of the operators around the SSD: leading dimensions and strides that are read and written where they lie, or
-refused. The elements around a slice hold NaN where it is read and a guard value where it is written."""
+refused, and offsets without sequences. The elements around a slice hold NaN where it is read and a guard value where it is written."""
+import ctypes
+import struct
+
 import pytest
 import torch
 
@@ -76,3 +79,36 @@ def test_rows_at_distance_zero():
     x = torch.randn(1, 1, 1, 64, generator=torch.Generator("cpu").manual_seed(3)).to(BF16).cuda()
     for shape in ((2, 6, 1, 64), (2, 1, 6, 64)):
         assert torch.equal(m.ssd_group_norm(x.expand(shape)), m.ssd_group_norm(x).expand(shape))
+
+
+def test_tokens_of_no_sequence_are_refused():
+    L = m.lib()
+    n = ctypes.c_size_t(0)
+    a = 1 << 20
+    scan = lambda seqlen: struct.pack("@5q4i", 0, seqlen, 64, 16, 1, 1, 0, 1, 1)  # noqa: E731
+    assert L.ssd_selective_scan_workspace_size(scan(0), ctypes.byref(n)) == 0
+    assert L.ssd_selective_scan_workspace_size(scan(5), ctypes.byref(n)) == 1
+    tensors = struct.pack("@12P12q", a, a, 0, a, a, a, a, 0, 0, 0, 0, a, 0, 64, 0, 64, 0, 0, 0, 16, 0, 16, 0, 64)
+    assert L.ssd_selective_scan(scan(5), tensors, a, 1 << 30, None) == 1
+    assert L.ssd_selective_scan(scan(0), tensors, a, 1 << 30, None) == 0
+    conv = lambda seqlen: struct.pack("@3q4i", 0, seqlen, 64, 4, 1, 1, 1)  # noqa: E731
+    tensors = struct.pack("@7P4q", a, 2 * a, a, 0, 0, 0, a, 0, 64, 0, 64)
+    assert L.ssd_conv(conv(5), tensors, None, None) == 1
+    assert L.ssd_conv(conv(0), tensors, None, None) == 0
+
+
+@gpu
+def test_offsets_of_no_sequences():
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w, A = torch.ones(64, 4, device="cuda"), -torch.ones(64, 16, device="cuda")
+    for L in (0, 5):
+        x, B = torch.ones(1, L, 64, device="cuda"), torch.ones(1, L, 1, 16, device="cuda")
+        if L:
+            with pytest.raises(ValueError, match="cu_seqlens"):
+                m.ssd_selective_scan(x, x, None, A, B, B, cu_seqlens=cu)
+            with pytest.raises(ValueError, match="cu_seqlens"):
+                m.ssd_conv(x, w, cu_seqlens=cu)
+        else:
+            y, f = m.ssd_selective_scan(x, x, None, A, B, B, cu_seqlens=cu)
+            o, c = m.ssd_conv(x, w, cu_seqlens=cu)
+            assert y.shape == o.shape == x.shape and f.shape == (0, 64, 16) and c.shape == (0, 64, 3)
