@@ -318,7 +318,8 @@ SSD_API ssd_status_t ssd_fwd_plan(const ssd_problem_t *prob, ssd_plan_t *plan);
  * Tensors of tokens are rows of `channels` contiguous elements; the row of
  * token t of sequence b starts at element b*seq + t*tok of the tensor, so a
  * column slice of wider rows needs no copy. Strides are in elements and may be
- * any (outputs' rows must not overlap). Pointers need the alignment of their
+ * any (outputs' rows must not overlap, each sequence's behind the one before or
+ * each token's). Pointers need the alignment of their
  * element only; rows on 16-byte boundaries run faster.
  *
  * `workspace` holds the 256-byte header that ssd_fwd_check reads (the device

@@ -23,10 +23,11 @@ bool fits(double a, double b, double c = 1.0) { return a * b * c <= 4e18; }
 bool strides_ok(int64_t seq, int64_t tok, int64_t nseq, int64_t L, int64_t width) {
     return seq >= 0 && tok >= 0 && (double)seq * (double)nseq + (double)tok * (double)L + (double)width <= 4e18;
 }
-// An output's rows must not overlap.
+// An output's rows must not overlap: each sequence's rows behind the one before, or each token's (token-major tensors).
 bool rows_apart(int64_t seq, int64_t tok, int64_t nseq, int64_t L, int64_t width) {
-    if (L > 1 && tok < width) return false;
-    return nseq <= 1 || seq >= (L > 1 ? (L - 1) * tok : 0) + width;
+    if (L <= 1) return nseq <= 1 || seq >= width;
+    if (nseq <= 1) return tok >= width;
+    return (tok >= width && seq >= (L - 1) * tok + width) || (seq >= width && tok >= (nseq - 1) * seq + width);
 }
 
 ssd_status_t check_scan(const ssd_scan_problem_t *p) {

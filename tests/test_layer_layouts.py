@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mamba_ssd_prefill_gb300 as m
+from test_layer_ops import conv_inputs, run_scan, scan_inputs
 
 gpu = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -112,3 +113,47 @@ def test_offsets_of_no_sequences():
             y, f = m.ssd_selective_scan(x, x, None, A, B, B, cu_seqlens=cu)
             o, c = m.ssd_conv(x, w, cu_seqlens=cu)
             assert y.shape == o.shape == x.shape and f.shape == (0, 64, 16) and c.shape == (0, 64, 3)
+
+
+def test_outputs_may_be_token_major_and_must_not_overlap():
+    """y [3, 5, 64]: a sequence's rows together, a token's rows together, with gaps; and rows that overlap. What passes the
+    checks of the arguments stops here for want of a GPU, or of memory at these addresses: only the checks are asked."""
+    L = m.lib()
+    if torch.cuda.is_available():
+        pytest.skip("addresses that are not the GPU's")
+    a = 1 << 20
+    problem = struct.pack("@5q4i", 3, 5, 64, 16, 1, 1, 0, 0, 1)
+    conv = struct.pack("@3q4i", 3, 5, 64, 4, 1, 1, 0)
+
+    def refused(seq, tok):
+        scan = L.ssd_selective_scan(problem, struct.pack("@12P12q", a, a, 0, a, a, a, a, 0, 0, 0, 0, 0, 0, 64, 0, 64, 0, 0,
+                                                         0, 16, 0, 16, seq, tok), a, 1 << 30, None)
+        assert (scan == 1) == (L.ssd_conv(conv, struct.pack("@7P4q", a, 2 * a, a, 0, 0, 0, 0, 0, 64, seq, tok), None,
+                                          None) == 1)
+        return scan == 1
+
+    for seq, tok in ((320, 64), (400, 70), (64, 192), (70, 300)):
+        assert not refused(seq, tok), (seq, tok)
+    for seq, tok in ((319, 64), (320, 63), (64, 191), (63, 192), (0, 64), (64, 64), (100, 150), (64, 0)):
+        assert refused(seq, tok), (seq, tok)
+
+
+@gpu
+@pytest.mark.parametrize("L", [1, 2, 75, 900])
+def test_token_major_tensors(L):
+    """[L, b, ..] tensors, seen as [b, L, ..]: read and written where they lie."""
+    t = scan_inputs(3, L, 72, 16, seed=5)
+    want = run_scan(t)
+    tm = lambda v: v.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    s = {k: tm(v) if k in ("x", "dt_raw", "B", "C", "z") else v for k, v in t.items()}
+    to = torch.full((L, 3, 90), GUARD, dtype=BF16, device="cuda")
+    y, f = run_scan(s, y=to.transpose(0, 1)[..., 8:80])
+    assert torch.equal(y, want[0]) and torch.equal(f, want[1])
+    y.fill_(GUARD)
+    assert bool((to == GUARD).all())
+    x, w, bias, state, _ = conv_inputs(3, L, 72, 4, seed=6)
+    want = m.ssd_conv(x, w, bias, state)
+    out, c = m.ssd_conv(tm(x), w, bias, state, out=to.transpose(0, 1)[..., 8:80])
+    assert torch.equal(out, want[0]) and torch.equal(c, want[1])
+    out.fill_(GUARD)
+    assert bool((to == GUARD).all())
