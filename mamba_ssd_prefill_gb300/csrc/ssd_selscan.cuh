@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
         if (SUM) {
             if (fresh) t0 = qb < t1 ? qb : t1;
             if (qe <= t1) {  // no sequence goes on past this segment
-                if (tid < left) p.seg_dt[item * p.D_ + c0 + tid] = __int_as_float(0x7fffffff);
+                for (int i = tid; i < left; i += NT) p.seg_dt[item * p.D_ + c0 + i] = __int_as_float(0x7fffffff);
                 return;
             }
         } else {

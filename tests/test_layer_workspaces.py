@@ -2,8 +2,9 @@
 import pytest
 import torch
 
+import layer_oracle as lo
 import mamba_ssd_prefill_gb300 as m
-from test_layer_ops import scan_inputs
+from test_layer_ops import ok, scan_inputs
 
 gpu = pytest.mark.gpu
 F32 = torch.float32
@@ -242,3 +243,42 @@ def test_one_workspace_for_the_ssd_and_the_operators_around_it():
         m.check(ws)
     assert e.value.status == 1
     m.check(ws)
+
+
+def sums_of_segments(ws, nseq, Dc, N, size):
+    """The steps' sums [segments, Dc] in a scan's workspace: behind the header and the segments' states, before a copy of
+    the initial states, each at a multiple of 256 bytes."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for items in range(1, 1 << 14):
+        sums = up(256 + items * Dc * N * 4)
+        if up(up(sums + items * Dc * 4) + nseq * Dc * N * 4) == size:
+            return ws[sums:sums + items * Dc * 4].view(F32).reshape(items, Dc)
+    raise AssertionError("no number of segments has this size")
+
+
+@gpu
+@pytest.mark.parametrize("N", [3, 4, 8, 16, 40])
+def test_every_segment_of_packed_sequences_has_a_sum_or_a_mark(N):
+    """Segments cut anywhere, also where one sequence ends and the next begins: each channel's sum of steps is written, or
+    NaN where no sequence goes on. Channels that fill one tile of the kernel and part of another."""
+    import ctypes
+    import struct
+
+    Dc, L = 150, 4096
+    lengths = [1024, 64, 960, 0, 1, 1023, 512, 512]
+    t = scan_inputs(1, L, Dc, N, lengths=lengths, seed=N)
+    n = ctypes.c_size_t(0)
+    problem = struct.pack("@5q4i", len(lengths), L, Dc, N, 1, 1, 0, 1, 1)
+    assert m.lib().ssd_selective_scan_workspace_size(problem, ctypes.byref(n)) == 0 and n.value > 256
+    ws = torch.full((n.value,), 0x5a, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    got = scan(t, workspace=ws)
+    m.check(ws)
+    sums = sums_of_segments(ws, len(lengths), Dc, N, n.value)
+    assert len(sums) > 20
+    assert not bool((sums.view(torch.int32) == 0x5a5a5a5a).any())
+    marked = torch.isnan(sums)
+    assert bool((marked == marked[:, :1]).all()) and bool((sums[~marked] > 0).all())
+    yr, fr, ey, ef = lo.scan(**t)
+    ok(got[0], yr, ey, t["x"].dtype)
+    ok(got[1], fr, ef, F32)
