@@ -496,7 +496,9 @@ PyObject *fp8_quantize(PyObject *const *a) {
     if (x.dim() < 1 || (block_rows == 128 && x.dim() != 2))
         throw Refusal{"x: expected [..., K], or a matrix [N, K] with block_rows=128"};
     const auto shape = x.sizes();
-    const int64_t K = shape.back(), n = K ? x.numel() / K : 0, kb = (K + 127) / 128;
+    const int64_t K = shape.back(), kb = (K + 127) / 128;
+    int64_t n = 1;  // rows, also of rows without elements
+    for (int64_t i = 0; i + 1 < x.dim(); ++i) n *= shape[i];
     const int64_t row = row_stride("x", x, shape, io, dev);
     Call call(dev, a[3], a[2], 256);
     const Tensor q = call.make(shape, at::kFloat8_e4m3fn);

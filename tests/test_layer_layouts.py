@@ -157,3 +157,13 @@ def test_token_major_tensors(L):
     assert torch.equal(out, want[0]) and torch.equal(c, want[1])
     out.fill_(GUARD)
     assert bool((to == GUARD).all())
+
+
+@gpu
+def test_a_product_of_rows_without_elements():
+    """K = 0: the scales of no blocks, by rows and by blocks of rows, as the product takes them."""
+    for M, N in ((40, 90), (3, 200), (1, 1)):
+        a, b = m.ssd_fp8_quantize(torch.zeros(M, 0, device="cuda")), m.ssd_fp8_quantize(torch.zeros(N, 0, device="cuda"), 128)
+        assert a[1].shape == (M, 0) and b[1].shape == (-(-N // 128), 0)
+        bias = torch.arange(float(N), device="cuda")
+        assert torch.equal(m.ssd_fp8_matmul(*a, *b, bias, out_dtype=torch.float32), bias.expand(M, N))
