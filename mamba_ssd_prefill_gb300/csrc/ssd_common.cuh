@@ -58,6 +58,7 @@ enum BoundsSite : uint32_t {
     SITE_RCONV_IN = 161, SITE_RCONV_OUT = 162, SITE_RCONV_STATE = 163,
     SITE_NORM_IN = 171, SITE_NORM_OUT = 172, SITE_NORM_SCALE = 173,
     SITE_FP8_IN = 181, SITE_FP8_OUT = 182, SITE_FP8_SCALE = 183,
+    SITE_OFFSETS = 191, SITE_WEIGHT = 192,  // of the operators around the SSD: cu_seqlens; fp32 vectors of channels
 };
 
 // Parameters common to the kernels. Element strides are implied by the packed

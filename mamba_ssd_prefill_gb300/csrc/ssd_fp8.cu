@@ -13,14 +13,16 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantParams p) {
     after_previous();
     const int lane = threadIdx.x % 32;
     const int64_t kb = (p.cols + 127) / 128, rb = (p.rows + p.block_rows - 1) / p.block_rows;
-    const IO *x = static_cast<const IO *>(p.x);
+    const int64_t xn = (p.rows - 1) * p.x_row + p.cols;
+    (void)xn;
     for (int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; w < rb * kb; w += (int64_t)gridDim.x * 8) {
         const int64_t r0 = w / kb * p.block_rows, c0 = w % kb * 128;
         const int64_t r1 = r0 + p.block_rows < p.rows ? r0 + p.block_rows : p.rows;
         const int n = (int)(p.cols - c0 < 128 ? p.cols - c0 : 128);
+        const IO *x = chk_rows(static_cast<const IO *>(p.x), r0 * p.x_row + c0, r1 - r0, p.x_row, n, xn, p.hdr, SITE_FP8_IN);
         float m = 0.f;
         for (int64_t r = r0; r < r1; ++r)
-            for (int i = lane; i < n; i += 32) m = max_nan(m, fabsf(to_f32(x[r * p.x_row + c0 + i])));
+            for (int i = lane; i < n; i += 32) m = max_nan(m, fabsf(to_f32(x[(r - r0) * p.x_row + i])));
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
         float scale, inv;
@@ -29,7 +31,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantParams p) {
         for (int64_t r = r0; r < r1; ++r)
             for (int i = lane; i < n; i += 32)
                 *chk(p.q, r * p.cols + c0 + i, 1, p.rows * p.cols, p.hdr, SITE_FP8_OUT) =
-                    (uint8_t)e4m3x2(to_f32(x[r * p.x_row + c0 + i]) * inv, 0.f);
+                    (uint8_t)e4m3x2(to_f32(x[(r - r0) * p.x_row + i]) * inv, 0.f);
     }
 }
 

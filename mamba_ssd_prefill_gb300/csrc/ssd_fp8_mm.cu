@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
             const Tile tl = wide_tile(t, mt, nt);
             const int64_t m = tl.m0 + q * 32 + lane, n0 = tl.n0 + half * 128;
             const bool live = m < p.m && n0 / 128 < nsb;
-            const float *sa = p.sa + (live ? m * nkb : 0), *sb = p.sb + (live ? n0 / 128 * nkb : 0);
+            const float *sa = chk(p.sa, live ? m * nkb : 0, nkb, p.m * nkb, hdr, SITE_FP8_SCALE);
+            const float *sb = chk(p.sb, live ? n0 / 128 * nkb : 0, nkb, nsb * nkb, hdr, SITE_FP8_SCALE);
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
@@ -255,7 +256,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 if (p.bias)
 #pragma unroll
                     for (int j = 0; j < CW; ++j)
-                        if (n0 + c * CW + j < p.n) acc[c * CW + j] += p.bias[n0 + c * CW + j];
+                        if (n0 + c * CW + j < p.n)
+                            acc[c * CW + j] += *chk(p.bias, n0 + c * CW + j, 1, p.n, hdr, SITE_WEIGHT);
                 if (vec) {  // the store before this one has read the buffer
                     if (lane == 0) bulk_wait_read0();
                     __syncwarp();
@@ -475,7 +477,10 @@ __global__ void __launch_bounds__(kNThreads)
         const int q = warp % 4, tid = threadIdx.x - 64;
         for (int e = tid; e < (kb1 - kb0) * TN; e += 128) {
             const int j = e % TN, kb = kb0 + e / TN;
-            scales[e] = m0 + j < p.m ? p.sa[(m0 + j) * nkb + kb] * p.sb[w0 / 128 * nkb + kb] : 0.f;
+            scales[e] = m0 + j < p.m
+                            ? *chk(p.sa, (m0 + j) * nkb + kb, 1, p.m * nkb, hdr, SITE_FP8_SCALE) *
+                                  *chk(p.sb, w0 / 128 * nkb + kb, 1, (p.n + 127) / 128 * nkb, hdr, SITE_FP8_SCALE)
+                            : 0.f;
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
         float2 acc[TN / 2];
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kNThreads)
             if (p.bias)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    if (x < left) o[x] += p.bias[n + x];
+                    if (x < left) o[x] += *chk(p.bias, n + x, 1, p.n, hdr, SITE_WEIGHT);
             OUT *out = chk(static_cast<OUT *>(p.out), (m0 + j) * p.out_row + n, left, (p.m - 1) * p.out_row + p.n, hdr,
                            SITE_FP8_OUT);
             if (vec && left == 4) {
@@ -571,7 +576,8 @@ template <typename OUT>
 __global__ void __launch_bounds__(256) bias_kernel(MatmulParams p) {
     after_previous();
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < p.m * p.n; e += (int64_t)gridDim.x * 256)
-        static_cast<OUT *>(p.out)[e / p.n * p.out_row + e % p.n] = from_f32<OUT>(p.bias ? p.bias[e % p.n] : 0.f);
+        *chk(static_cast<OUT *>(p.out), e / p.n * p.out_row + e % p.n, 1, (p.m - 1) * p.out_row + p.n, p.hdr,
+             SITE_FP8_OUT) = from_f32<OUT>(p.bias ? *chk(p.bias, e % p.n, 1, p.n, p.hdr, SITE_WEIGHT) : 0.f);
 }
 
 // 2-D map over [rows, k] bytes, box [box_rows, 128 bytes], 128-byte swizzle, zeros outside

@@ -218,9 +218,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// `count` rows of `width` elements `stride` apart, the first at element idx of a buffer of n: their address. The bounds-checked
+// builds look at the whole span, and at nothing where there are no rows.
+template <typename T>
+__device__ __forceinline__ T *chk_rows(T *base, int64_t idx, int64_t count, int64_t stride, int64_t width, int64_t n,
+                                       WsHeader *hdr, uint32_t site) {
+#ifdef SSD_BOUNDS_CHECK
+    return count > 0 && width > 0 ? chk(base, idx, (count - 1) * stride + width, n, hdr, site) : base;
+#else
+    return base + idx;
+#endif
+}
+
 // Packed sequences: the token range of sequence s, kept inside [0, T] whatever the offsets hold.
-__device__ __forceinline__ void packed_range(const int32_t *cu, int64_t s, int64_t T, int64_t &begin, int64_t &end) {
-    const int64_t b = cu[s], e = cu[s + 1];
+__device__ __forceinline__ void packed_range(const int32_t *cu, int64_t nseq, int64_t s, int64_t T, WsHeader *hdr,
+                                             int64_t &begin, int64_t &end) {
+    const int32_t *at = chk(cu, s, 2, nseq + 1, hdr, SITE_OFFSETS);
+    const int64_t b = at[0], e = at[1];
     begin = b < 0 ? 0 : b > T ? T : b;
     end = e < begin ? begin : e > T ? T : e;
 }

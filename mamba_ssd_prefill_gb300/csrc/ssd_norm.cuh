@@ -37,8 +37,13 @@ __global__ void __launch_bounds__(kThreads) norm_long_kernel(NormParams p) {
     const int64_t gs = p.D / p.G;
     for (int64_t item = blockIdx.x; item < p.rows * p.G; item += gridDim.x) {
         const int64_t row = item / p.G, c0 = (item % p.G) * gs;
-        const IO *x = static_cast<const IO *>(p.x) + row * p.x_row + c0;
-        const IO *z = p.z ? static_cast<const IO *>(p.z) + row * p.z_row + c0 : nullptr;
+        const IO *x = chk(static_cast<const IO *>(p.x), row * p.x_row + c0, gs, (p.rows - 1) * p.x_row + p.D, p.hdr,
+                          SITE_NORM_IN);
+        const IO *z = !p.z ? nullptr
+                           : chk(static_cast<const IO *>(p.z), row * p.z_row + c0, gs, (p.rows - 1) * p.z_row + p.D,
+                                 p.hdr, SITE_NORM_IN);
+        const int64_t yn = (p.rows - 1) * p.y_row + p.D;
+        (void)yn;
         auto act = [&](float v) { return p.silu ? silu_f32(v) : v; };
         auto in = [&](int64_t i) {
             const float v = to_f32(x[i]);
@@ -58,14 +63,15 @@ __global__ void __launch_bounds__(kThreads) norm_long_kernel(NormParams p) {
         const float r = rsqrtf(block_sum(s, red) / (float)gs + p.eps);
         auto value = [&](int64_t i) {
             const int64_t c = c0 + i;
-            const float v = fmaf((in(i) - mean) * r, p.w ? p.w[c] : 1.f, p.bias ? p.bias[c] : 0.f);
+            const float v = fmaf((in(i) - mean) * r, p.w ? *chk(p.w, c, 1, p.D, p.hdr, SITE_WEIGHT) : 1.f,
+                                 p.bias ? *chk(p.bias, c, 1, p.D, p.hdr, SITE_WEIGHT) : 0.f);
             return !z ? act(v) : p.gate_first ? v : v * act(to_f32(z[i]));
         };
         if (!p.scales) {
-            IO *y = static_cast<IO *>(p.y) + row * p.y_row + c0;
+            IO *y = chk(static_cast<IO *>(p.y), row * p.y_row + c0, gs, yn, p.hdr, SITE_NORM_OUT);
             for (int64_t i = threadIdx.x; i < gs; i += kThreads) y[i] = from_f32<IO>(value(i));
         } else {  // a warp takes a block of 128 channels, four a lane
-            uint8_t *y = static_cast<uint8_t *>(p.y) + row * p.y_row + c0;
+            uint8_t *y = chk(static_cast<uint8_t *>(p.y), row * p.y_row + c0, gs, yn, p.hdr, SITE_NORM_OUT);
             const int lane = threadIdx.x % 32;
             for (int64_t b = threadIdx.x / 32; b * 128 < gs; b += kThreads / 32) {
                 float v[4], m = 0.f;
@@ -217,7 +223,8 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) norm_kernel(NormParams p, 
         const int64_t ci = c0 + e0 * V, yi = row * p.y_row + ci;
         // weight and bias of a pair's channels (only read where they exist: i < mine)
         auto scale_shift = [&](int i, float2 *o) {
-            const float *wp = p.w + ci + i * apart * V, *bp = p.bias + ci + i * apart * V;
+            const float *wp = chk(p.w, ci + i * apart * V, V, p.D, p.hdr, SITE_WEIGHT);
+            const float *bp = chk(p.bias, ci + i * apart * V, V, p.D, p.hdr, SITE_WEIGHT);
             if constexpr (V == 1) {
                 if (p.w) o[0].x *= __ldg(wp);
                 if (p.bias) o[0].x += __ldg(bp);

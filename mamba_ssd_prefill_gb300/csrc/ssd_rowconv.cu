@@ -45,7 +45,7 @@ __device__ __forceinline__ Walk walk_of(const RowConvParams &p, int64_t item, in
         w.t0 = item * tl;
         w.t1 = w.t0 + tl < p.T ? w.t0 + tl : p.T;
         w.s = seq_of(p.cu, p.nseq, w.t0);
-        packed_range(p.cu, w.s, p.T, w.start, w.end);
+        packed_range(p.cu, p.nseq, w.s, p.T, p.hdr, w.start, w.end);
         if (w.start > w.t0) w.start = w.t0;  // malformed offsets
         if (w.end <= w.t0) w.end = p.T + 1;
     } else {
@@ -62,7 +62,7 @@ __device__ __forceinline__ Walk walk_of(const RowConvParams &p, int64_t item, in
 __device__ __forceinline__ void next_sequence(const RowConvParams &p, Walk &w, int64_t t) {
     do {
         if (++w.s >= p.nseq) break;
-        packed_range(p.cu, w.s, p.T, w.start, w.end);
+        packed_range(p.cu, p.nseq, w.s, p.T, p.hdr, w.start, w.end);
     } while (w.end <= t);
     if (w.s >= p.nseq) w.s = p.nseq - 1, w.start = t, w.end = p.T + 1;  // malformed offsets
 }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 7 ? 2 : K > 4 ? 3 :
     };
     if (p.cu && write_state && K > 1)  // empty sequences keep their cache; each tile's threads look after some of them
         for (int64_t q = item; q < p.nseq; q += tiles)
-            if (p.cu[q] == p.cu[q + 1]) {
+            if (const int32_t *o = chk(p.cu, q, 2, p.nseq + 1, p.hdr, SITE_OFFSETS); o[0] == o[1]) {
                 load_hist(q, 0, 0);
                 save(q);
             }
@@ -190,19 +190,20 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 8 : K > 7 ? 2 : K > 4 ? 3 :
     for (int i = 0; i < V; ++i) {
         float t[K];
         const int64_t ci = i < live ? c + i : c;
+        const float *wc = chk(p.w, ci * K, K, p.D * K, p.hdr, SITE_WEIGHT);
         if constexpr (K == 4) {
             if (p.vec_w) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(p.w + ci * 4));
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(wc));
                 t[0] = u.x, t[1] = u.y, t[2] = u.z, t[3] = u.w;
             } else {
 #pragma unroll
-                for (int j = 0; j < K; ++j) t[j] = p.w[ci * K + j];
+                for (int j = 0; j < K; ++j) t[j] = wc[j];
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < K; ++j) t[j] = p.w[ci * K + j];
+            for (int j = 0; j < K; ++j) t[j] = wc[j];
         }
-        const float b = p.bias ? p.bias[ci] : 0.f;
+        const float b = p.bias ? *chk(p.bias, ci, 1, p.D, p.hdr, SITE_WEIGHT) : 0.f;
 #pragma unroll
         for (int j = 0; j < K; ++j)
             if (i % 2) w[j][i / 2].y = t[j];
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) row_conv_state_kernel(RowConvParams 
     for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kThreads) {
         const int64_t s = e / p.D, c = e % p.D;
         int64_t row0 = 0, end = p.L;
-        if (p.cu) packed_range(p.cu, s, p.T, row0, end);
+        if (p.cu) packed_range(p.cu, p.nseq, s, p.T, p.hdr, row0, end);
         IO v[7];
 #pragma unroll
         for (int j = 0; j < 7; ++j) {

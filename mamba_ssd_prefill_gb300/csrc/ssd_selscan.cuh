@@ -150,12 +150,14 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
         t1 = t0 + p.seg_len < p.T ? t0 + p.seg_len : p.T;
         int64_t qb;
         sq = seq_at(p.cu, p.nseq, SUM ? t1 - 1 : t0);
-        packed_range(p.cu, sq, p.T, qb, qe);
+        packed_range(p.cu, p.nseq, sq, p.T, p.hdr, qb, qe);
         fresh = qb >= t0;
         if (SUM) {
             if (fresh) t0 = qb < t1 ? qb : t1;
             if (qe <= t1) {  // no sequence goes on past this segment
-                for (int i = tid; i < left; i += NT) p.seg_dt[item * p.D_ + c0 + i] = __int_as_float(0x7fffffff);
+                for (int i = tid; i < left; i += NT)
+                    *chk(p.seg_dt, item * p.D_ + c0 + i, 1, p.seg_items * p.D_, p.hdr, SITE_SCAN_SEG) =
+                        __int_as_float(0x7fffffff);
                 return;
             }
         } else {
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
             if (item == 0 && ct == 0) check_offsets(p.cu, p.nseq, p.T, p.hdr);
             if (p.fin)  // empty sequences keep their states; each segment's CTAs look after some of them
                 for (int64_t s = item; s < p.nseq; s += p.nseg)
-                    if (p.cu[s] == p.cu[s + 1])
+                    if (const int32_t *o = chk(p.cu, s, 2, p.nseq + 1, p.hdr, SITE_OFFSETS); o[0] == o[1])
                         for (int64_t e = tid; e < left * p.N; e += NT) {
                             const int64_t i = (s * p.D_ + c0) * p.N + e;
                             store_state(p, p.fin, i, p.init ? load_state(p, p.init, i) : 0.f);
@@ -269,8 +271,8 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
     load(t0, 0);
 
     for (int i = tid; i < CT; i += NT) {
-        bias_s[i] = p.dt_bias && i < left ? p.dt_bias[c0 + i] : 0.f;
-        D_s[i] = p.D && i < left ? p.D[c0 + i] : 0.f;
+        bias_s[i] = p.dt_bias && i < left ? *chk(p.dt_bias, c0 + i, 1, p.D_, p.hdr, SITE_WEIGHT) : 0.f;
+        D_s[i] = p.D && i < left ? *chk(p.D, c0 + i, 1, p.D_, p.hdr, SITE_WEIGHT) : 0.f;
     }
     f2 a[kCH][P], h[kCH][P];
     const int n0 = q * R;
@@ -299,8 +301,8 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
                 h[c][j / 2 + 1] = pack2(w.x, w.y);
             }
     };
-    if (vec_rows) get_rows(p.A, c0 + ch, p.D_ * p.N, SITE_SCAN_STATE);
-    else get2([&](int64_t c, int n) { return p.A[c * p.N + n]; });
+    if (vec_rows) get_rows(p.A, c0 + ch, p.D_ * p.N, SITE_WEIGHT);
+    else get2([&](int64_t c, int n) { return *chk(p.A, c * p.N + n, 1, p.D_ * p.N, p.hdr, SITE_WEIGHT); });
 #pragma unroll
     for (int c = 0; c < kCH; ++c)
 #pragma unroll
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
                     int64_t qb = 0;
                     do {
                         if (++sq >= p.nseq) break;
-                        packed_range(p.cu, sq, p.T, qb, qe);
+                        packed_range(p.cu, p.nseq, sq, p.T, p.hdr, qb, qe);
                     } while (qe <= tile + e);
                     if (sq >= p.nseq) {  // the end, or malformed offsets
                         sq = p.nseq - 1;
@@ -543,7 +545,8 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
 #pragma unroll
         for (int c = 0; c < kCH; ++c)
             if (q == 0 && c < clive)
-                p.seg_dt[i0 * p.D_ + c0 + ch + c] = packed && fresh ? __int_as_float(0x7fffffff) : dt_sum[c];
+                *chk(p.seg_dt, i0 * p.D_ + c0 + ch + c, 1, p.seg_items * p.D_, p.hdr, SITE_SCAN_SEG) =
+                    packed && fresh ? __int_as_float(0x7fffffff) : dt_sum[c];
     } else if (!packed && t1 == p.L) {
         final_state(sq);
     }
@@ -567,7 +570,7 @@ static __global__ void __launch_bounds__(kJoinChains *kJoinThreads) join_kernel(
         base = quick_div(e, dn, i) * segs;
         c = quick_div(i, p.N, rest);
     }
-    const float a = live ? p.A[i] * kLog2e : 0.f;
+    const float a = live ? *chk(p.A, i, 1, dn, p.hdr, SITE_WEIGHT) * kLog2e : 0.f;
     const int64_t extent = p.seg_items * dn;
     (void)extent;
     // (d, v) leaves h as exp(a d) h + v; as v where d is NaN: a segment in which a sequence begins
@@ -579,7 +582,8 @@ static __global__ void __launch_bounds__(kJoinChains *kJoinThreads) join_kernel(
         const int n = !live || j0 >= segs ? 0 : (int)(segs - j0 < kJoin ? segs - j0 : kJoin);
         float v[kJoin], d[kJoin];
         float *s = chk(p.seg_state, n ? (base + j0) * dn + i : 0, n ? (n - 1) * dn + 1 : 0, extent, p.hdr, SITE_SCAN_SEG);
-        const float *sd = p.seg_dt + (n ? (base + j0) * p.D_ + c : 0);
+        const float *sd = chk_rows(p.seg_dt, n ? (base + j0) * p.D_ + c : 0, n, p.D_, 1, p.seg_items * p.D_, p.hdr,
+                                   SITE_SCAN_SEG);
 #pragma unroll
         for (int j = 0; j < kJoin; ++j) {
             v[j] = d[j] = 0.f;
@@ -634,13 +638,16 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
     const int64_t total = p.nseq * p.D_ * p.N, seq_states = p.D_ * p.N;
     (void)total;
     const bool whole = nl >= R;
+    const int mine_n = whole ? R : nl < 0 ? 0 : nl;
+    (void)mine_n;
     after_previous();
     const int mine = q * kSeqs / S;  // this lane discretises and gates for the sequences mine, mine + 1, ..
     const int64_t i0 = s0 * seq_states + cN + n0;
-    const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, Dc = p.D ? p.D[cc] : 0.f;
+    const float bias = p.dt_bias ? *chk(p.dt_bias, cc, 1, p.D_, p.hdr, SITE_WEIGHT) : 0.f;
+    const float Dc = p.D ? *chk(p.D, cc, 1, p.D_, p.hdr, SITE_WEIGHT) : 0.f;
     float a[R];
 #pragma unroll
-    for (int k = 0; k < R; ++k) a[k] = k < nl ? p.A[cN + n0 + k] * kLog2e : 0.f;
+    for (int k = 0; k < R; ++k) a[k] = k < nl ? *chk(p.A, cN + n0 + k, 1, p.D_ * p.N, p.hdr, SITE_WEIGHT) * kLog2e : 0.f;
 
     // FAST: all of the group's sequences and of this lane's states exist, and whole vectors are aligned
     auto body = [&](auto fast) {
@@ -649,7 +656,7 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
         Raw<IO, R> rb[kSeqs], rc[kSeqs];
         const ST *init = static_cast<const ST *>(p.init);
         if (init) {
-            const ST *hp = chk(init, i0, FAST ? R : nl < 0 ? 0 : nl < R ? nl : R, total, p.hdr, SITE_SCAN_STATE);
+            const ST *hp = chk_rows(init, i0, ns, seq_states, mine_n, total, p.hdr, SITE_SCAN_STATE);
 #pragma unroll
             for (int j = 0; j < kSeqs; ++j) {
                 if constexpr (FAST) {
@@ -665,9 +672,12 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
         }
         float x[PER], d[PER], z[PER], u[PER];
         {
-            const IO *xp = static_cast<const IO *>(p.x) + (s0 + mine) * p.x_seq + cc;
-            const IO *dp = static_cast<const IO *>(p.dt) + (s0 + mine) * p.dt_seq + cc;
-            const IO *zp = p.z ? static_cast<const IO *>(p.z) + (s0 + mine) * p.z_seq + cc : nullptr;
+            auto rows = [&](const void *q, int64_t seq) {  // this channel in the lane's sequences
+                return chk_rows(static_cast<const IO *>(q), (s0 + mine) * seq + cc, ns - mine < PER ? ns - mine : PER,
+                                seq, 1, (p.rows - 1) * seq + p.D_, p.hdr, SITE_SCAN_IN);
+            };
+            const IO *xp = rows(p.x, p.x_seq), *dp = rows(p.dt, p.dt_seq);
+            const IO *zp = p.z ? rows(p.z, p.z_seq) : nullptr;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 x[j] = d[j] = z[j] = 0.f;
@@ -679,8 +689,11 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
             }
         }
         {
-            const IO *B = static_cast<const IO *>(p.B) + s0 * p.b_seq + g * p.N + n0;
-            const IO *C = static_cast<const IO *>(p.C) + s0 * p.c_seq + g * p.N + n0;
+            auto rows = [&](const void *q, int64_t seq) {  // this lane's states in the sequences
+                return chk_rows(static_cast<const IO *>(q), s0 * seq + g * p.N + n0, ns, seq, mine_n,
+                                (p.rows - 1) * seq + p.G * p.N, p.hdr, SITE_SCAN_IN);
+            };
+            const IO *B = rows(p.B, p.b_seq), *C = rows(p.C, p.c_seq);
 #pragma unroll
             for (int j = 0; j < kSeqs; ++j) {
                 if constexpr (FAST) {
@@ -703,7 +716,7 @@ __global__ void __launch_bounds__(128) step_kernel(ScanParams p) {
         }
         float v[kSeqs];
         ST *fp = static_cast<ST *>(p.fin);
-        if (fp) fp = chk(fp, i0, FAST ? R : nl < 0 ? 0 : nl < R ? nl : R, total, p.hdr, SITE_SCAN_STATE);
+        if (fp) fp = chk_rows(fp, i0, ns, seq_states, mine_n, total, p.hdr, SITE_SCAN_STATE);
 #pragma unroll
         for (int j = 0; j < kSeqs; ++j) {
             const int src = j * S / kSeqs;  // the lane that discretised for sequence j

@@ -167,3 +167,22 @@ def test_a_product_of_rows_without_elements():
         assert a[1].shape == (M, 0) and b[1].shape == (-(-N // 128), 0)
         bias = torch.arange(float(N), device="cuda")
         assert torch.equal(m.ssd_fp8_matmul(*a, *b, bias, out_dtype=torch.float32), bias.expand(M, N))
+
+
+@gpu
+def test_bounds_checked_build_reports_no_violation_in_these_layouts():
+    import os
+    import subprocess
+    import sys
+
+    from mamba_ssd_prefill_gb300 import _build
+
+    path = _build.build(checked=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, os.path.join(here, "layer_bounds_layouts.py")], capture_output=True, text=True,
+                       env={**os.environ, "MAMBA_SSD_LIB": path}, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = [ln.split() for ln in r.stdout.splitlines()]
+    at = lines.index(["--", "0"])  # the other list's cases come first
+    bad = [ln for ln in lines if ln[-1] != "0"]
+    assert len(lines) - at > 200 and not bad, bad
