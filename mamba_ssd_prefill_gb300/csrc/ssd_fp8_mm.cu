@@ -603,8 +603,10 @@ cudaError_t launch_wide(const MatmulParams &p, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k, smem, done);
     if (e != cudaSuccess) return e;
-    // output map [m, n], box [32, 128 bytes], where rows lie on 16-byte boundaries
-    int vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_row * sizeof(OUT))) & 15) == 0;
+    // output map [m, n], box [32, 128 bytes], where rows lie on 16-byte boundaries and are made of whole 16-byte pieces: a TMA
+    // store clips by pieces, and wrote the rest of a last one over what lies behind column n of wider rows
+    int vec = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_row * sizeof(OUT)) |
+                (uintptr_t)(p.n * sizeof(OUT))) & 15) == 0;
     CUtensorMap mo = ma;
     if (vec) {
         const cuuint64_t dims[2] = {(cuuint64_t)p.n, (cuuint64_t)p.m};

@@ -186,3 +186,20 @@ def test_bounds_checked_build_reports_no_violation_in_these_layouts():
     at = lines.index(["--", "0"])  # the other list's cases come first
     bad = [ln for ln in lines if ln[-1] != "0"]
     assert len(lines) - at > 200 and not bad, bad
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [4001, 4002, 3996, 4000])
+def test_products_into_wider_rows_leave_what_lies_behind(dtype, N):
+    """Many rows (the kernel of 128 x 256 tiles), N columns of rows on 16-byte boundaries, whole 16-byte pieces or not."""
+    g = torch.Generator("cpu").manual_seed(N)
+    a = m.ssd_fp8_quantize(torch.randn(1300, 640, generator=g).cuda())
+    b = m.ssd_fp8_quantize(torch.randn(N, 640, generator=g).cuda(), 128)
+    want = m.ssd_fp8_matmul(*a, *b, out_dtype=dtype)
+    for off, wide in ((0, 4016), (8, 4024), (16, 4032)):
+        to = torch.full((1300, wide), GUARD, dtype=dtype, device="cuda")
+        out = m.ssd_fp8_matmul(*a, *b, out_dtype=dtype, out=to[:, off:off + N])
+        assert torch.equal(out, want)
+        out.fill_(GUARD)
+        assert bool((to == GUARD).all())
