@@ -468,6 +468,17 @@ SSD_API ssd_status_t ssd_fp8_matmul(const ssd_matmul_problem_t *prob, const void
                                     const void *b, const float *b_scales, const float *bias, void *out,
                                     int64_t out_row, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Process-wide test hook, as ssd_debug_knobs: forces the kernel of later
+ * ssd_fp8_matmul calls, for tests that compare each with the oracle.
+ *  token_tile  -1 the library's own choice (with splits -1); 0 the kernel of
+ *              128 x 256 tiles; 16, 32, 64 or 128 the one for few tokens, with
+ *              as many to a tile
+ *  splits      CTAs that share K: 1, 2, 4 or 8 (1 for token_tile 0)
+ * Anything else is SSD_ERR_INVALID_ARG and changes nothing. A call whose problem
+ * the forced kernel does not hold (fewer blocks of K than splits, more than
+ * 3840 scales a CTA) returns SSD_ERR_UNSUPPORTED. */
+SSD_API ssd_status_t ssd_debug_product(int32_t token_tile, int32_t splits);
+
 /* Static text for a status code. */
 SSD_API const char *ssd_status_string(ssd_status_t status);
 

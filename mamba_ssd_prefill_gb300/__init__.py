@@ -15,7 +15,7 @@ import threading
 
 import torch
 
-__all__ = ["ssd_fwd", "ssd_fwd_host", "ssd_fwd_varlen", "ssd_fwd_conv", "workspace_size", "make_problem", "check", "debug_set", "debug_knobs", "kernel_for", "plan_info", "SsdError",
+__all__ = ["ssd_fwd", "ssd_fwd_host", "ssd_fwd_varlen", "ssd_fwd_conv", "workspace_size", "make_problem", "check", "debug_set", "debug_knobs", "debug_product", "kernel_for", "plan_info", "SsdError",
            "Workspace", "lib", "LIB_PATH", "STATUS", "ssd_selective_scan", "ssd_conv", "ssd_group_norm",
            "ssd_fp8_quantize", "ssd_fp8_matmul"]
 
@@ -101,6 +101,8 @@ def lib():
             L.ssd_fp8_quantize.restype = ctypes.c_int
             L.ssd_fp8_matmul.argtypes = [vp] * 7 + [i64, vp, sz, vp]
             L.ssd_fp8_matmul.restype = ctypes.c_int
+            L.ssd_debug_product.argtypes = [ctypes.c_int32] * 2
+            L.ssd_debug_product.restype = ctypes.c_int
             L.ssd_status_string.argtypes = [ctypes.c_int]
             L.ssd_status_string.restype = ctypes.c_char_p
             L.ssd_version.argtypes = []
@@ -464,6 +466,13 @@ def debug_knobs(tc_heads_per_unit=-1, tc_late_ticket=-1, simt_two_pass=-1, conv_
                                int(tc_segment_chunks), int(tc_head_flags))
     if st:
         raise SsdError(st, "ssd_debug_knobs")
+
+
+def debug_product(token_tile=-1, splits=-1):
+    """Test hook: force the kernel of later ssd_fp8_matmul calls (-1, -1 restores the library's own choice)."""
+    st = lib().ssd_debug_product(int(token_tile), int(splits))
+    if st:
+        raise SsdError(st, "ssd_debug_product")
 
 
 from .layer import ssd_conv, ssd_fp8_matmul, ssd_fp8_quantize, ssd_group_norm, ssd_selective_scan  # noqa: E402

@@ -691,13 +691,23 @@ Choice choose(const MatmulParams &p, int sms) {
     return best;
 }
 
+std::atomic<int> forced_tile{-1}, forced_splits{-1};  // ssd_debug_product; -1: the library's own choice
+bool runs(const MatmulParams &p, Choice c) {  // whether a forced choice holds the problem
+    if (c.tn == 0) return c.splits == 1;
+    const int64_t nkb = (p.k + kBK - 1) / kBK, mt = (p.m + c.tn - 1) / c.tn;
+    return c.splits <= nkb && (nkb + c.splits - 1) / c.splits * c.tn <= kNScales && mt <= 65535 &&
+           mt * ((p.n + 127) / 128) * c.splits <= (1 << 30);
+}
+
 template <typename OUT>
 cudaError_t launch_t(const MatmulParams &p, int sms, cudaStream_t stream) {
     if (p.k == 0) {
         return launch_after(bias_kernel<OUT>, std::min<int64_t>((p.m * p.n + 255) / 256, (int64_t)sms * 8), 256, 0, stream,
                             p);
     }
-    const Choice c = choose(p, sms);
+    const Choice forced{forced_tile.load(std::memory_order_relaxed), forced_splits.load(std::memory_order_relaxed)};
+    if (forced.tn >= 0 && !runs(p, forced)) return cudaErrorNotSupported;
+    const Choice c = forced.tn >= 0 ? forced : choose(p, sms);
     switch (c.tn) {
         case 16: return launch_narrow<OUT, 16>(p, c.splits, stream);
         case 32: return launch_narrow<OUT, 32>(p, c.splits, stream);
@@ -708,6 +718,16 @@ cudaError_t launch_t(const MatmulParams &p, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
+
+bool force_product(int token_tile, int splits) {
+    const bool own = token_tile == -1 && splits == -1;
+    const bool narrow = (token_tile == 16 || token_tile == 32 || token_tile == 64 || token_tile == 128) &&
+                        (splits == 1 || splits == 2 || splits == 4 || splits == 8);
+    if (!own && !narrow && !(token_tile == 0 && splits == 1)) return false;
+    forced_splits.store(splits, std::memory_order_relaxed);
+    forced_tile.store(token_tile, std::memory_order_relaxed);
+    return true;
+}
 
 cudaError_t launch_matmul(const MatmulParams &p, int out_dtype, int sms, cudaStream_t stream) {
     if (out_dtype == SSD_F32) return launch_t<float>(p, sms, stream);

@@ -178,6 +178,8 @@ struct MatmulParams {
     WsHeader *hdr;
     int64_t m, n, k, out_row;
 };
+// cudaErrorNotSupported: the forced kernel and split (ssd_debug_product) do not run this problem
 cudaError_t launch_matmul(const MatmulParams &p, int out_dtype, int sms, cudaStream_t stream);
+bool force_product(int token_tile, int splits);  // false: no such kernel
 
 }  // namespace ssd

@@ -403,8 +403,12 @@ SSD_API ssd_status_t ssd_fp8_matmul(const ssd_matmul_problem_t *prob, const void
     p.n = pr.n;
     p.k = pr.k;
     p.out_row = out_row;
-    return ssd::launch_matmul(p, pr.out_dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK
-                                                                                                     : SSD_ERR_CUDA;
+    const cudaError_t e = ssd::launch_matmul(p, pr.out_dtype, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : e == cudaErrorNotSupported ? SSD_ERR_UNSUPPORTED : SSD_ERR_CUDA;
+}
+
+SSD_API ssd_status_t ssd_debug_product(int32_t token_tile, int32_t splits) {
+    return ssd::force_product(token_tile, splits) ? SSD_OK : SSD_ERR_INVALID_ARG;
 }
 
 }  // extern "C"
