@@ -155,9 +155,13 @@ __global__ void __launch_bounds__(T::NT, UNIT ? T::MINB : T::MINB_SINGLE) scan_k
         if (SUM) {
             if (fresh) t0 = qb < t1 ? qb : t1;
             if (qe <= t1) {  // no sequence goes on past this segment
-                for (int i = tid; i < left; i += NT)
-                    *chk(p.seg_dt, item * p.D_ + c0 + i, 1, p.seg_items * p.D_, p.hdr, SITE_SCAN_SEG) =
-                        __int_as_float(0x7fffffff);
+                auto mark = [&](int i) {  // (a loop from tid on made the prompts' passes 1.7 % slower: 742 against 729 us)
+                    if (i < left)
+                        *chk(p.seg_dt, item * p.D_ + c0 + i, 1, p.seg_items * p.D_, p.hdr, SITE_SCAN_SEG) =
+                            __int_as_float(0x7fffffff);
+                };
+#pragma unroll
+                for (int i = 0; i < CT; i += NT) mark(tid + i);
                 return;
             }
         } else {
