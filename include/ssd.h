@@ -444,9 +444,11 @@ SSD_API ssd_status_t ssd_group_norm(const ssd_norm_problem_t *prob, const ssd_no
 /* e4m3 values with one fp32 scale per block of block_rows x 128 elements of
  * x [rows, cols]: with m the block's largest magnitude, scale = m / 448 and
  * q = round-to-nearest-even(x * (448 / m)) (m = 0: scale 1). A block that holds
- * an infinity or a NaN gets the scale NaN. block_rows is 1 (activations: one
- * scale per token and 128 channels) or 128 (weights). q [rows, cols] and
- * scales [ceil(rows / block_rows), ceil(cols / 128)] are contiguous. */
+ * an infinity or a NaN gets the scale NaN. 448 / m is at most the largest finite
+ * number, so a block with m below 1.3e-36 comes back smaller than it was.
+ * block_rows is 1 (activations: one scale per token and 128 channels) or 128
+ * (weights). q [rows, cols] and scales [ceil(rows / block_rows),
+ * ceil(cols / 128)] are contiguous. */
 SSD_API ssd_status_t ssd_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, int32_t io_dtype, const void *x,
                                       int64_t x_row, void *q, float *scales, void *workspace, void *stream);
 

@@ -492,6 +492,6 @@ SSD_API const char *ssd_status_string(ssd_status_t status) {
     return "unknown status";
 }
 
-SSD_API int ssd_version(void) { return 10200; }
+SSD_API int ssd_version(void) { return 10300; }
 
 }  // extern "C"

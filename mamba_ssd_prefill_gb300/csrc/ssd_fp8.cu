@@ -1,6 +1,7 @@
 // The quantiser of the e4m3 projections: one scale per block of 128 columns and one row (activations) or 128 rows
 // (weights); include/ssd.h has the formulas. HBM-bound: with rows of 8-element pieces 16 lanes hold a block of one row
-// in registers from its one read to its write. Weights, quantised once, and other rows are read twice.
+// in registers from its one read to its write (16384 x 2560 bf16: 26 us, 4.8 TB/s). Weights, quantised once, and other rows
+// are read twice, an element a lane (10576 x 2560: fp32 319 us, bf16 193; rows of 2561 bf16 elements 105).
 #include "ssd_internal.h"
 #include "ssd_layer.cuh"
 

@@ -7,9 +7,12 @@
 // tensor cores work on the next block in the other half of TMEM.
 //
 // Two kernels. wide_kernel: tokens are the 128 rows (TMEM lanes) of a tile, 256 weights its columns; one persistent
-// CTA per SM, TMA into four stages of 48 KB, two blocks in TMEM. What bounds it is the turn of a TMEM half: MMA (512
-// clocks), read, FMA and back, so a warp reads 64 columns at a time and gives the half back before it adds them (16
-// columns at a time 16384 x 10576 x 2560 took 369 us, so 341: 2.6 PFLOP/s, under the power cap; 16384 x 8192 x 8192: 2.8).
+// CTA per SM, TMA into four stages of 48 KB, two blocks in TMEM (256 columns each). What bounds it is the turn of a TMEM
+// half: MMA (512 clocks), read, FMA and back, so a warp reads 64 columns at a time and gives the half back before it adds
+// the last 64 (16 columns at a time 16384 x 10576 x 2560 took 369 us, so 341 to 348: 2.6 PFLOP/s; 16384 x 8192 x 8192:
+// 2.9). The tensor pipe is active for 52 % of the time (4096 x 10576 x 2560). In seconds of such products the power limit
+// takes the SM clock to 1.75 GHz and the time to 382 us; at that clock a full pipe would take 211.
+// fp32 output writes twice the bytes: 563 us with a bias.
 // narrow_kernel, for few tokens: weights are the 128 rows and TN tokens the columns, so no row of the tensor core idles;
 // K is split over the CTAs of a cluster, whose partial sums are joined through distributed shared memory in rank order
 // (no atomics: the result does not depend on timing). 16 x 10576 x 2560: 7.3 us, the weights at 3.7 TB/s.
@@ -623,8 +626,8 @@ cudaError_t launch_wide(const MatmulParams &p, int sms, cudaStream_t stream) {
             vec = 0;
     }
     // Many waves start once the kernel before has ended: started as its CTAs leave, the CTAs of neighbouring tiles land on
-    // SMs apart (quantiser and product, 16384 x 2560 x 10576: 410 us against 401; 8191 x 5120 x 2560 behind the norm,
-    // four waves: 157 against 160).
+    // SMs apart (quantiser and product, 16384 x 2560 x 10576, 35 waves: 410 us against 401; 8191 x 5120 x 2560 behind the
+    // norm, four waves: 157 against 160). Nothing was measured between the two; the switch stands at twice the smaller.
     if (tiles < (int64_t)sms * 8) return launch_after(k, std::min<int64_t>(tiles, sms), kWThreads, smem, stream, p, ma, mb, mo, vec);
     k<<<(unsigned)sms, kWThreads, smem, stream>>>(p, ma, mb, mo, vec);
     return cudaGetLastError();

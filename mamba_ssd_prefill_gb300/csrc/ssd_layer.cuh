@@ -202,7 +202,8 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
 }
 
 // Scale of a block whose largest magnitude is m (NaN where the block holds a NaN or an infinity), and the factor
-// its values are multiplied with. A subnormal m would make 448 / m infinite: the largest finite factor is taken.
+// its values are multiplied with. Below m = 1.3e-36 the quotient 448 / m is infinite and the largest finite factor is
+// taken instead: such a block comes back too small.
 constexpr float kE4m3Max = 448.f;
 __device__ __forceinline__ void e4m3_scale(float m, float &scale, float &inv) {
     if (m == 0.f) {

@@ -62,10 +62,12 @@ ScanPlan plan_scan(const ssd_scan_problem_t &p, int sms, bool segments, bool sin
     // Without segments the work of a chain runs once, with them its states' part twice. So segments are cut only where
     // the CTAs leave the SMs short of warps (under about 1.3 CTAs of 128 threads each: 4 x 4096 x 1536 x 16, 48 CTAs,
     // 0.84 ms in one chain and 0.24 segmented; 32 x 4096 x 1536 x 16, 384 CTAs, 1.28 and 1.57 ms when both were
-    // measured), and then so many that the resident CTAs are full once, or twice where segments are long: a part of a
-    // wave leaves SMs idle (8192 x 5120 x 16: 0.5, 1, 1.5 and 2 waves 0.70, 0.378, 0.416 and 0.379 ms; 16384 x 5120 x 16:
-    // 1 and 2 waves 0.736 and 0.728), and more segments pay their entry more often (4000 x 1536 x 16, packed: 1 and 2
-    // waves 75 and 85 us).
+    // measured in one build), and then so many that the resident CTAs are full about once, or twice where segments are
+    // long: a part of a wave leaves SMs idle (8192 x 5120 x 16: 0.5, 1, 1.5 and 2 waves 0.70, 0.378, 0.416 and 0.379 ms;
+    // 16384 x 5120 x 16: 1 and 2 waves 0.736 and 0.728), and more segments pay their entry more often (4000 x 1536 x 16,
+    // packed: 1 and 2 waves 75 and 85 us). The segments of one wave are rounded down and then doubled, so the waves are
+    // whole only where a segment has few CTAs: 16 x 4096 x 1536 x 16 has 192, 6 segments and 1.52 waves (908 us; 12
+    // sequences 671, 24 1289).
     const ssd::ScanCta cta = ssd::scan_cta(p.dstate);
     const int64_t per_group = (p.channels / p.ngroups + cta.channels - 1) / cta.channels;
     const int64_t ctas = chains * p.ngroups * per_group, threads = ctas * cta.threads;

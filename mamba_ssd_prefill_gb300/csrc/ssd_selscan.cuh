@@ -16,9 +16,12 @@
 //    load costs its bytes per lane, broadcast or not (an LDS.128 four cycles of the SM's pipe), and B and C are eight
 //    bytes for every element: with one channel a thread they took 3.4 cycles an element and bounded the kernel. CH = 4,
 //    R = 8 (128 registers) and CH = 2, R = 8 (96) measure the same where segments fill the GPU (16384 x 5120 x 16:
-//    0.73 ms); where they are not needed the smaller one has more warps (32 x 4096 x 1536 x 16: 1.75 ms against 1.28
-//    when both were measured, now 1.48) and is taken. Up to 8 states a tile is 4 tokens and not 8, which 16 tiles an SM would not fit in shared memory
-//    (4 x 4096 x 1536 x 4: 131 us against 178; 12824 x 4000 x 8: 330 against 380).
+//    0.73 ms); where they are not needed the smaller one has more warps and is taken (32 x 4096 x 1536 x 16, both in one
+//    build: CH = 4 1.75 ms, CH = 2 1.28; the present build takes 1.48). Up to 8 states a tile is 4 tokens and not 8, of
+//    which fewer CTAs would fit in shared memory (4 x 4096 x 1536 x 4: 131 us against 178; 12824 x 4000 x 8: 330
+//    against 380).
+//  - States are padded to 4, 8, 16, 24, 32, 64, 128 or 256: 4 x 4096 x 1536 with 32 states takes 437 us, with 33 1035,
+//    with 64 932, with 128 1689, with 256 3186.
 //  - The sum over a channel's lanes is taken for the thread's channels at once, each shuffle halving the channels a
 //    lane holds.
 //
