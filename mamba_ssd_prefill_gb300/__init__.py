@@ -162,8 +162,10 @@ class Workspace:
         self.held = []          # smaller buffers that captured graphs use
         self.layer = None       # the Workspace of the operators around the SSD
 
-    def get(self, nbytes: int) -> torch.Tensor:
-        capturing = torch.cuda.is_current_stream_capturing()
+    def get(self, nbytes: int, capturing=None) -> torch.Tensor:
+        """`capturing`: whether a graph is being captured on the stream of the call (None: on the current one)."""
+        if capturing is None:
+            capturing = torch.cuda.is_current_stream_capturing()
         if self.buf is None or self.buf.numel() < nbytes:
             # the library asks for a zero-filled workspace on first use only
             nbytes = max(nbytes, 256)
@@ -187,12 +189,13 @@ class Workspace:
             self.buf.zero_()  # on the current stream, ordered before the call that uses it
         return self.buf
 
-    def get_layer(self, nbytes: int) -> torch.Tensor:
+    def get_layer(self, nbytes: int, capturing=None) -> torch.Tensor:
         """The same for the operators around the SSD, in a buffer apart: the scan keeps its segments' states where
         ssd_fwd expects the tags that its calls left."""
-        if self.layer is None:
-            self.layer = Workspace(self.device)
-        return self.layer.get(nbytes)
+        layer = self.layer
+        if layer is None:
+            layer = self.layer = Workspace(self.device)
+        return layer.get(nbytes, capturing)
 
     def buffers(self) -> list:
         """Every buffer that calls may have reported to."""

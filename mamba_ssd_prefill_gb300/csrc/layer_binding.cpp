@@ -223,7 +223,12 @@ struct Call {
         const int is_workspace = PyObject_IsInstance(workspace, workspace_class);
         if (is_workspace < 0) throw Raised{};
         if (is_workspace) {
-            PyObject *t = PyObject_CallMethod(workspace, "get_layer", "n", (Py_ssize_t)bytes);
+            static PyObject *get_layer = PyUnicode_InternFromString("get_layer");
+            PyObject *n = PyLong_FromSize_t(bytes);
+            if (!n || !get_layer) throw Raised{};
+            PyObject *args[3] = {workspace, n, capturing() ? Py_True : Py_False};
+            PyObject *t = PyObject_VectorcallMethod(get_layer, args, 3, nullptr);
+            Py_DECREF(n);
             if (!t) throw Raised{};
             if (THPVariable_Check(t)) ws = THPVariable_Unpack(t);
             Py_DECREF(t);
@@ -232,6 +237,11 @@ struct Call {
         }
         if (!ws.defined() || !ws.is_cuda() || ws.get_device() != dev || !ws.is_contiguous())
             throw Refusal{"workspace: expected a Workspace, or a contiguous tensor on the tensors' device"};
+    }
+    bool capturing() const {
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        cuda_ok(cudaStreamIsCapturing(stream.stream(), &capture), "the workspace");
+        return capture != cudaStreamCaptureStatusNone;
     }
     // The workspace of a call that is given none. A graph that is being captured gets scratch of its own, from its own
     // memory: the stream's workspace may be replaced by a larger one while the graph lives, and graphs captured on one
@@ -243,9 +253,7 @@ struct Call {
             ws = status;
             return;
         }
-        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-        cuda_ok(cudaStreamIsCapturing(stream.stream(), &capture), "the workspace");
-        if (capture != cudaStreamCaptureStatusNone) {
+        if (capturing()) {
             of_capture = true;
             ws = make({(int64_t)bytes}, at::kByte);
             ws.narrow(0, 0, status.numel()).zero_();
