@@ -147,9 +147,10 @@ def kernel_for(prob: SsdProblem) -> str:
 class Workspace:
     """A zero-initialised device workspace, grown on demand and reused across calls on one stream.
 
-    A buffer that a captured graph uses lives as long as the Workspace, also when a later call needs a larger one, and
-    one that is first needed inside a capture is zeroed at once, outside of the graph. Graphs captured with one
-    Workspace must not be replayed at the same time. Calls of the SSD and of the operators around it may share one."""
+    A buffer that a captured graph uses lives as long as the Workspace, also when a later call needs a larger one: keep the
+    Workspace as long as the graph, like its other tensors. One that is first needed inside a capture is of the graph's
+    own memory, and zeroed at once too. Graphs captured with one Workspace must not be replayed at the same time. Calls of
+    the SSD and of the operators around it may share one."""
 
     # the state-passing tags carry the launch count modulo 2^22: the buffer is zero-filled again well before that
     REZERO_EVERY = 1 << 21
@@ -168,14 +169,11 @@ class Workspace:
             capturing = torch.cuda.is_current_stream_capturing()
         if self.buf is None or self.buf.numel() < nbytes:
             # the library asks for a zero-filled workspace on first use only
-            nbytes = max(nbytes, 256)
-            if capturing:
+            new = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            if capturing:  # zeroed by each replay, whose own memory it is, and now for the calls before the first
                 from . import layer
 
-                index = torch.cuda.current_device() if self.device.index is None else self.device.index
-                new = layer._bind().zeros_outside(nbytes, index)
-            else:
-                new = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+                layer._bind().zero_now(new)
             if self.buf is not None:
                 if capturing or self.in_graphs:
                     self.held.append(self.buf)

@@ -8,7 +8,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/from_blob.h>
 #include <ATen/ops/maximum.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -143,29 +142,30 @@ void cuda_ok(cudaError_t e, const char *what) {
     }
 }
 
-// Zeroed memory that is none of PyTorch's, also while a graph is being captured: it lies outside of the graph's memory and
-// is zeroed now, not at each replay. Freed with the tensor. Called with the device current.
-Tensor zeros_outside(int64_t bytes, int dev) {
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;  // an allocation beside a capture
-    cuda_ok(cudaThreadExchangeStreamCaptureMode(&mode), "a workspace");
-    void *p = nullptr;
-    cudaStream_t s = nullptr;
-    cudaError_t e = cudaMalloc(&p, (size_t)bytes);
-    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
-    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, (size_t)bytes, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (s) (void)cudaStreamDestroy(s);
-    if (e != cudaSuccess && p) (void)cudaFree(p);
-    (void)cudaThreadExchangeStreamCaptureMode(&mode);
-    cuda_ok(e, "a workspace");
-    auto release = [](void *q) {
-        cudaStreamCaptureMode m = cudaStreamCaptureModeRelaxed;
-        const bool changed = cudaThreadExchangeStreamCaptureMode(&m) == cudaSuccess;
-        (void)cudaFree(q);
-        if (changed) (void)cudaThreadExchangeStreamCaptureMode(&m);
-    };
-    return at::from_blob(p, {bytes}, release,
-                         at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+// Calls beside a capture that the capture's mode would forbid on this thread (allocations, waits for other streams).
+struct Relaxed {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    Relaxed() { cuda_ok(cudaThreadExchangeStreamCaptureMode(&mode), "a workspace"); }
+    ~Relaxed() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+bool is_capturing(const c10::cuda::CUDAStream &stream) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cuda_ok(cudaStreamIsCapturing(stream.stream(), &capture), "a workspace");
+    return capture != cudaStreamCaptureStatusNone;
+}
+
+// A stream of PyTorch's that no graph is being captured on.
+c10::cuda::CUDAStream stream_apart(int dev) {
+    for (int i = 0; i < 64; ++i) {
+        const auto side = c10::cuda::getStreamFromPool(false, (c10::DeviceIndex)dev);
+        if (!is_capturing(side)) return side;
+    }
+    throw std::runtime_error("a workspace: every stream is being captured");
+}
+// Zeroes a tensor now, whatever is being captured. Called with its device current.
+void zero_now(const Tensor &t, const c10::cuda::CUDAStream &side) {
+    cuda_ok(cudaMemsetAsync(t.data_ptr(), 0, t.nbytes(), side.stream()), "a workspace");
+    cuda_ok(cudaStreamSynchronize(side.stream()), "a workspace");
 }
 
 std::map<int, Tensor> &device_headers() {
@@ -177,7 +177,15 @@ std::map<int, Tensor> &device_headers() {
 // of the graph. Called with the device current.
 const Tensor &device_status(int dev) {
     Tensor &t = device_headers()[dev];
-    if (!t.defined()) t = zeros_outside(256, dev);
+    if (!t.defined()) {
+        const Relaxed relaxed;
+        const auto side = stream_apart(dev);  // no memory of a graph's
+        const c10::cuda::CUDAStreamGuard on(side);
+        const Tensor header =
+            at::empty({256}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+        zero_now(header, side);
+        t = header;
+    }
     return t;
 }
 Tensor status_word(const Tensor &header) { return header.narrow(0, 12, 4).view(at::kInt); }
@@ -226,7 +234,7 @@ struct Call {
             static PyObject *get_layer = PyUnicode_InternFromString("get_layer");
             PyObject *n = PyLong_FromSize_t(bytes);
             if (!n || !get_layer) throw Raised{};
-            PyObject *args[3] = {workspace, n, capturing() ? Py_True : Py_False};
+            PyObject *args[3] = {workspace, n, is_capturing(stream) ? Py_True : Py_False};
             PyObject *t = PyObject_VectorcallMethod(get_layer, args, 3, nullptr);
             Py_DECREF(n);
             if (!t) throw Raised{};
@@ -238,11 +246,6 @@ struct Call {
         if (!ws.defined() || !ws.is_cuda() || ws.get_device() != dev || !ws.is_contiguous())
             throw Refusal{"workspace: expected a Workspace, or a contiguous tensor on the tensors' device"};
     }
-    bool capturing() const {
-        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-        cuda_ok(cudaStreamIsCapturing(stream.stream(), &capture), "the workspace");
-        return capture != cudaStreamCaptureStatusNone;
-    }
     // The workspace of a call that is given none. A graph that is being captured gets scratch of its own, from its own
     // memory: the stream's workspace may be replaced by a larger one while the graph lives, and graphs captured on one
     // stream may be replayed on several. A captured call of the scan so takes two small nodes more (the header zeroed,
@@ -253,7 +256,7 @@ struct Call {
             ws = status;
             return;
         }
-        if (capturing()) {
+        if (is_capturing(stream)) {
             of_capture = true;
             ws = make({(int64_t)bytes}, at::kByte);
             ws.narrow(0, 0, status.numel()).zero_();
@@ -585,20 +588,18 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// zeros_outside(bytes, device index), for the Workspace class
-PyObject *zeros(PyObject *, PyObject *const *args, Py_ssize_t n) {
+// zero_now(tensor), for the Workspace class
+PyObject *zero(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 2) {
-        PyErr_Format(PyExc_TypeError, "expected 2 arguments, got %zd", n);
+    if (n != 1 || !THPVariable_Check(args[0])) {
+        PyErr_SetString(PyExc_TypeError, "expected a tensor");
         return nullptr;
     }
-    try {
-        const int64_t bytes = whole(args[0]), dev = whole(args[1]);
-        c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        return THPVariable_Wrap(zeros_outside(bytes, (int)dev));
-    } catch (const Raised &) {
-        return nullptr;
-    }
+    const Tensor &t = THPVariable_Unpack(args[0]);
+    const c10::cuda::CUDAGuard guard(t.device());
+    const Relaxed relaxed;
+    zero_now(t, stream_apart(t.get_device()));
+    Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
 
@@ -660,7 +661,7 @@ template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)> PyMethodDef
 }
 PyMethodDef methods[] = {
     method<bind>("bind"),
-    method<zeros>("zeros_outside"),
+    method<zero>("zero_now"),
     method<reported>("reported"),
     method<entry<selective_scan, 17>>("selective_scan"),
     method<entry<conv, 11>>("conv"),

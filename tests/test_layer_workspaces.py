@@ -282,3 +282,26 @@ def test_every_segment_of_packed_sequences_has_a_sum_or_a_mark(N):
     yr, fr, ey, ef = lo.scan(**t)
     ok(got[0], yr, ey, t["x"].dtype)
     ok(got[1], fr, ef, F32)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["ssd", "scan"])
+def test_memory_of_a_capture_outlives_its_workspace(kind):
+    """What a Workspace takes inside a capture is the graph's: it stays when the Workspace goes."""
+    want = [o.clone() for o in call_of(kind, m.Workspace("cuda"))()]
+    ws = m.Workspace("cuda")
+    call = call_of(kind, ws)
+    inputs = call.__closure__  # the graph reads them
+    side = torch.cuda.Stream()
+    graph, out = captured(call, side)
+    at, size = ws.buffers()[-1].data_ptr(), ws.buffers()[-1].numel()
+    pools = [tuple(s["segment_pool_id"]) for s in torch.cuda.memory_snapshot()
+             if s["address"] <= at < s["address"] + s["total_size"]]
+    assert pools and pools[0] != (0, 0)
+    ws.held, ws.buf, ws.layer = [], None, None
+    torch.cuda.empty_cache()
+    fillers = [torch.full((size // 4,), 3.0, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(o, w) for o, w in zip(out, want))
+    assert inputs and all(bool((f == 3).all()) for f in fillers)
